@@ -224,8 +224,8 @@ def prepare(case, seed):
         st["shape"] = moe.attn_shape(T=T, B=B, Hq=Hq, Hkv=Hkv, D=D, kv_dtype=case["kv"],
                                      page_size=page, max_pages=st["block_table"].shape[1],
                                      num_pages=num_pages, **more)
-        st["ws"] = torch.zeros(moe.moe_attn_workspace_size(st["shape"]), dtype=torch.uint8,
-                               device=DEV)
+        st["ws"] = torch.zeros(moe.moe_attn_workspace_size(st["shape"], case["op"] == "prefill"),
+                               dtype=torch.uint8, device=DEV)
     return st
 
 
