@@ -218,6 +218,97 @@ MOE_API moe_status moe_forward(const moe_shape* shape, const void* x, const void
                                int32_t* expert_offsets, int32_t* perm_token, int32_t* inv_slot,
                                float* y_perm, void* y, void* ws, size_t ws_bytes, void* stream);
 
+/* ---- attention over a paged key-value cache -------------------------------------------------
+ * The other half of a decoder layer, between the qkv projection and the output projection:
+ * moe_attn_append norms and rotates a step's queries and keys and writes keys and values into
+ * the cache; moe_attn_decode (one new token per sequence) and moe_attn_prefill (any number)
+ * attend over it. Hq = G * Hkv query heads, G per key head; head h * G + g reads key head h.
+ *
+ * Sequence b holds kv_len[b] cached tokens, this step's included, in the pages
+ * block_table[b, 0 ..]: cache place j lies in page block_table[b, j / page_size] at row
+ * j % page_size. Its new tokens are rows q_start[b] .. q_start[b+1]-1 of q, k, v and o; the i-th
+ * of n has place kv_len[b] - n + i (a negative place is padding: nothing is cached for it and
+ * its output is zero). Place p sees place j if j <= p and (window = 0 or p - j < window or
+ * j < n_sink). block_table entries of pages that hold no visible place are not read; what the
+ * cache holds beyond kv_len or outside the window never reaches a result.
+ *
+ * q_start, kv_len, block_table and positions are DEVICE int32 arrays and are checked there: a
+ * page outside [0, num_pages), a length beyond the table or a rotary position outside
+ * [0, max_pos) is recorded as MOE_ERR_DEVICE_BOUNDS and the access is skipped. Two sequences
+ * must not append to the same place. */
+typedef enum {
+  MOE_KV_BF16 = 0,          /* cache of bf16 keys and values                                  */
+  MOE_KV_FP8_E4M3 = 1       /* cache of E4M3 codes, one fp32 scale per key head               */
+} moe_kv_dtype;
+
+typedef struct {
+  int32_t T;          /* new tokens in the step, all sequences together (decode: T = B)       */
+  int32_t B;          /* sequences                                                            */
+  int32_t Hq, Hkv;    /* query heads and key heads; Hq a multiple of Hkv, Hq / Hkv <= 128     */
+  int32_t D;          /* head width: 64 or 128                                                */
+  int32_t kv_dtype;   /* moe_kv_dtype of the cache                                            */
+  int32_t page_size;  /* tokens of a page, >= 1                                               */
+  int32_t max_pages;  /* columns of block_table                                               */
+  int32_t num_pages;  /* pages of the cache                                                   */
+  int32_t window;     /* 0: every earlier place is visible; else the last `window` places     */
+  int32_t n_sink;     /* with a window: the first n_sink places stay visible                  */
+  int32_t rot_dim;    /* leading elements of a head that are rotated: a multiple of 16, <= D  */
+  int32_t rot_pairs;  /* 0: element i turns with i + rot_dim/2; 1: element 2i with 2i + 1     */
+  int32_t max_pos;    /* rows of cos_sin                                                      */
+  float scale;        /* softmax scale; 0 means 1 / sqrt(D)                                   */
+  float eps;          /* of the norms                                                         */
+  /* Strides in elements; 0 means packed. Every stride is a multiple of 16 bytes.             */
+  int64_t q_stride, k_stride, v_stride;   /* append's inputs, between tokens (Hq*D, Hkv*D)    */
+  int64_t qr_stride;                      /* append's q_out, the attentions' q (Hq*D)         */
+  int64_t o_stride;                       /* the attentions' o (Hq*D)                         */
+  /* both caches: between pages, between key heads, between tokens of a page. Packed is
+   * [num_pages, Hkv, page_size, D]; [num_pages, page_size, Hkv, D] is head_stride = D,
+   * token_stride = Hkv * D, page_stride = page_size * Hkv * D. */
+  int64_t page_stride, head_stride, token_stride;
+} moe_attn_shape;
+
+/* Bytes of scratch for moe_attn_append and moe_attn_decode, or (prefill != 0) for
+ * moe_attn_prefill as well; 0 for an invalid shape. The first moe_attn_workspace_zero_bytes()
+ * bytes (the device status word and the counters that the attentions leave at zero) must be
+ * zero before the first call; nothing else needs initialisation, and one workspace may serve
+ * several shapes. moe_check_device_status reads its status word. */
+MOE_API size_t moe_attn_workspace_size(const moe_attn_shape* shape, int prefill);
+MOE_API size_t moe_attn_workspace_zero_bytes(void);
+
+/* Norms, rotation and cache append in one pass over a step's projections.
+ *   q [T, Hq, D], k [T, Hkv, D], v [T, Hkv, D] bf16 (token strides q_stride, k_stride, v_stride:
+ *     they may be parts of one projection's rows).
+ *   q_norm, k_norm [D] bf16, or NULL for no norm: y = x / sqrt(mean(x^2) + eps) * norm, per head.
+ *   cos_sin [max_pos, rot_dim] fp32: the cosines of the rot_dim/2 angles, then the sines; (a, b)
+ *     becomes (a cos - b sin, b cos + a sin). NULL if rot_dim = 0.
+ *   positions [T] int32 rotary positions, or NULL for the tokens' places in the cache.
+ *   q_start [B+1], or NULL with T = B for one new token per sequence. Rows from q_start[B] on
+ *     are padding.
+ *   k_scale, v_scale [Hkv] fp32 (E4M3 caches; NULL for 1, and for bf16 caches): the cache holds
+ *     e4m3(value / scale), rounded to nearest even and saturating at +-448.
+ *   q_out [T, Hq, D] bf16 out (may be q itself if the strides agree); k_cache, v_cache updated.
+ * The arithmetic is fp32 with one rounding at the end. */
+MOE_API moe_status moe_attn_append(const moe_attn_shape* shape, const void* q, const void* k,
+                                   const void* v, const void* q_norm, const void* k_norm,
+                                   const float* cos_sin, const int32_t* positions,
+                                   const int32_t* block_table, const int32_t* kv_len,
+                                   const int32_t* q_start, const float* k_scale,
+                                   const float* v_scale, void* q_out, void* k_cache,
+                                   void* v_cache, void* ws, size_t ws_bytes, void* stream);
+
+/* Attention of one new token per sequence (T = B) over the cache.
+ *   s_j = scale * q . k_j over the visible places, o = sum_j softmax(s)_j v_j, lse = ln sum_j e^s_j
+ *   q [B, Hq, D] bf16, o [B, Hq, D] bf16 out, lse [B, Hq] fp32 out or NULL.
+ * A sequence with kv_len = 0 gives o = 0 and lse = -inf. Scores, the softmax's maximum and sum
+ * and the output are held in fp32; the probabilities enter the product with v as f16 (E4M3 cache)
+ * or as the sum of two bf16 (bf16 cache). The result does not depend on the order in which blocks
+ * run. */
+MOE_API moe_status moe_attn_decode(const moe_attn_shape* shape, const void* q,
+                                   const void* k_cache, const void* v_cache,
+                                   const float* k_scale, const float* v_scale,
+                                   const int32_t* block_table, const int32_t* kv_len, void* o,
+                                   float* lse, void* ws, size_t ws_bytes, void* stream);
+
 /* Reads (and clears) the first device-side error recorded in `ws` since the last check.
  * Synchronises `stream`. Returns MOE_OK, MOE_ERR_DEVICE_BOUNDS or MOE_ERR_DEVICE_TIMEOUT (or
  * MOE_ERR_CUDA if the read itself fails). */

@@ -16,10 +16,15 @@ __all__ = ["MoeError", "MoeShape", "MOE_W_BF16", "MOE_W_FP8_E4M3_B128", "MOE_W_M
            "moe_expert_ffn", "moe_combine", "moe_forward",
            "moe_check_device_status", "moe_selftest_bounded_wait", "moe_profile_enable",
            "moe_profile_read",
-           "moe_last_error_string", "shape_of", "MoeLayer", "EXPORTED"]
+           "moe_last_error_string", "shape_of", "MoeLayer", "EXPORTED",
+           "MoeAttnShape", "MOE_KV_BF16", "MOE_KV_FP8_E4M3", "attn_shape",
+           "moe_attn_workspace_size", "moe_attn_workspace_zero_bytes", "moe_attn_append",
+           "moe_attn_decode"]
 
 MOE_W_BF16, MOE_W_FP8_E4M3_B128, MOE_W_MXFP4_E8M0_B32 = 0, 1, 2
 WDTYPES = {"bf16": MOE_W_BF16, "fp8": MOE_W_FP8_E4M3_B128, "mxfp4": MOE_W_MXFP4_E8M0_B32}
+MOE_KV_BF16, MOE_KV_FP8_E4M3 = 0, 1
+KV_DTYPES = {"bf16": MOE_KV_BF16, "fp8": MOE_KV_FP8_E4M3}
 STATUS = {0: "MOE_OK", -1: "MOE_ERR_INVALID_ARG", -2: "MOE_ERR_UNSUPPORTED",
           -3: "MOE_ERR_WORKSPACE", -4: "MOE_ERR_CUDA", -5: "MOE_ERR_DEVICE_TIMEOUT",
           -6: "MOE_ERR_DEVICE_BOUNDS"}
@@ -27,7 +32,9 @@ EXPORTED = ("moe_workspace_size", "moe_route", "moe_route_hash", "moe_route_noal
             "moe_expert_ffn",
             "moe_combine", "moe_forward",
             "moe_check_device_status", "moe_selftest_bounded_wait", "moe_profile_enable",
-            "moe_profile_read", "moe_last_error_string")
+            "moe_profile_read", "moe_last_error_string",
+            "moe_attn_workspace_size", "moe_attn_workspace_zero_bytes", "moe_attn_append",
+            "moe_attn_decode")
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 
@@ -46,6 +53,16 @@ class MoeShape(ctypes.Structure):
     _fields_ = [("T", ctypes.c_int32), ("d", ctypes.c_int32), ("E", ctypes.c_int32),
                 ("k", ctypes.c_int32), ("f", ctypes.c_int32), ("n_shared", ctypes.c_int32),
                 ("wdtype", ctypes.c_int32)]
+
+
+class MoeAttnShape(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_int32) for n in
+                 ("T", "B", "Hq", "Hkv", "D", "kv_dtype", "page_size", "max_pages", "num_pages",
+                  "window", "n_sink", "rot_dim", "rot_pairs", "max_pos")]
+                + [("scale", ctypes.c_float), ("eps", ctypes.c_float)]
+                + [(n, ctypes.c_int64) for n in
+                   ("q_stride", "k_stride", "v_stride", "qr_stride", "o_stride", "page_stride",
+                    "head_stride", "token_stride")])
 
 
 _lib = None
@@ -88,6 +105,15 @@ def load():
     L.moe_profile_read.restype = i32
     L.moe_profile_read.argtypes = [ctypes.POINTER(ctypes.c_double), ctypes.POINTER(ctypes.c_double),
                                    ctypes.POINTER(ctypes.c_int64), ctypes.POINTER(ctypes.c_int64)]
+    ashp = ctypes.POINTER(MoeAttnShape)
+    L.moe_attn_workspace_size.restype = sz
+    L.moe_attn_workspace_size.argtypes = [ashp, i32]
+    L.moe_attn_workspace_zero_bytes.restype = sz
+    L.moe_attn_workspace_zero_bytes.argtypes = []
+    L.moe_attn_append.restype = i32
+    L.moe_attn_append.argtypes = [ashp] + [vp] * 16 + [sz, vp]
+    L.moe_attn_decode.restype = i32
+    L.moe_attn_decode.argtypes = [ashp] + [vp] * 10 + [sz, vp]
     L.moe_last_error_string.restype = ctypes.c_char_p
     L.moe_last_error_string.argtypes = []
     _lib = L
@@ -218,6 +244,49 @@ def moe_profile_read() -> dict:
                                    ctypes.byref(launches)), "moe_profile_read")
     return {"ms_gate_up": up.value, "ms_down": dn.value, "ffn_calls": calls.value,
             "kernel_launches": launches.value}
+
+
+def attn_shape(T, B, Hq, Hkv, D, kv_dtype="bf16", page_size=16, max_pages=1, num_pages=1,
+               window=0, n_sink=0, rot_dim=0, rot_pairs=False, max_pos=0, scale=0.0, eps=1e-6,
+               q_stride=0, k_stride=0, v_stride=0, qr_stride=0, o_stride=0, page_stride=0,
+               head_stride=0, token_stride=0) -> MoeAttnShape:
+    """moe_attn_shape; a scale or stride of 0 is the default (1/sqrt(D), packed)."""
+    if isinstance(kv_dtype, str):
+        kv_dtype = KV_DTYPES[kv_dtype]
+    return MoeAttnShape(T, B, Hq, Hkv, D, kv_dtype, page_size, max_pages, num_pages, window,
+                        n_sink, rot_dim, int(rot_pairs), max_pos, scale, eps, q_stride, k_stride,
+                        v_stride, qr_stride, o_stride, page_stride, head_stride, token_stride)
+
+
+def moe_attn_workspace_size(shape: MoeAttnShape, prefill: bool = False) -> int:
+    return int(load().moe_attn_workspace_size(ctypes.byref(shape), int(prefill)))
+
+
+def moe_attn_workspace_zero_bytes() -> int:
+    return int(load().moe_attn_workspace_zero_bytes())
+
+
+def moe_attn_append(shape, q, k, v, q_norm, k_norm, cos_sin, positions, block_table, kv_len,
+                    q_start, k_scale, v_scale, q_out, k_cache, v_cache, ws, stream=None,
+                    ws_bytes=None):
+    """Per-head norms, rotation and append to the paged cache; q_out is the rotated q."""
+    wp, wb = _ws(ws)
+    _check(load().moe_attn_append(ctypes.byref(shape), _ptr(q), _ptr(k), _ptr(v), _ptr(q_norm),
+                                  _ptr(k_norm), _ptr(cos_sin), _ptr(positions),
+                                  _ptr(block_table), _ptr(kv_len), _ptr(q_start), _ptr(k_scale),
+                                  _ptr(v_scale), _ptr(q_out), _ptr(k_cache), _ptr(v_cache), wp,
+                                  wb if ws_bytes is None else ws_bytes, _stream(stream)),
+           "moe_attn_append")
+
+
+def moe_attn_decode(shape, q, k_cache, v_cache, k_scale, v_scale, block_table, kv_len, o, lse, ws,
+                    stream=None, ws_bytes=None):
+    """Attention of one new token per sequence over the paged cache."""
+    wp, wb = _ws(ws)
+    _check(load().moe_attn_decode(ctypes.byref(shape), _ptr(q), _ptr(k_cache), _ptr(v_cache),
+                                  _ptr(k_scale), _ptr(v_scale), _ptr(block_table), _ptr(kv_len),
+                                  _ptr(o), _ptr(lse), wp, wb if ws_bytes is None else ws_bytes,
+                                  _stream(stream)), "moe_attn_decode")
 
 
 class MoeLayer:

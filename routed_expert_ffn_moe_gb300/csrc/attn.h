@@ -1,0 +1,100 @@
+// Internal interface of the attention operators: resolved dimensions, workspace, launchers.
+#pragma once
+
+#include "internal.h"
+
+namespace moe {
+
+// n / d for 0 <= n < 2^31 by one multiplication: m = ceil(2^p / d) with p = 31 + ceil(log2 d).
+struct FastDiv {
+  uint32_t d, m, p;
+};
+
+inline FastDiv fast_div(uint32_t d) {
+  FastDiv f{d, 0, 31};
+  while ((1ull << (f.p - 31)) < d) ++f.p;
+  f.m = (uint32_t)(((1ull << f.p) + d - 1) / d);
+  return f;
+}
+
+// moe_attn_shape with every default filled in
+struct AttnDims {
+  int T, B, Hq, Hkv, G, D;
+  int fp8;
+  int page_size, max_pages, num_pages;
+  int window, n_sink;  // window 0: none (n_sink then 0)
+  int rot_dim, rot_pairs, max_pos;
+  float scale, eps;
+  int64_t q_stride, k_stride, v_stride, qr_stride, o_stride;
+  int64_t page_stride, head_stride, token_stride;
+  FastDiv page_div;
+};
+
+// ---- workspace -----------------------------------------------------------------------------
+//   status    int32[64]               device error code (first error wins)
+//   counters  int32[kAttnMaxCtas]     decode: arrivals at each split item; every call leaves
+//                                     them at zero
+//   parts     f32 [2 * ctas][16][D]   decode: unnormalised outputs of split items
+//   ml        f32 [2 * ctas][16][2]   decode: their running maxima and sums
+constexpr int kAttnMaxCtas = 2048;
+constexpr size_t kAttnZeroBytes = 256 + (size_t)kAttnMaxCtas * 4;
+constexpr int kDecodeRows = 16;  // query heads of one decode item
+
+struct AttnWs {
+  size_t status, counters, parts, ml, total;
+};
+
+inline AttnWs attn_ws(const AttnDims& a, int prefill) {
+  AttnWs L{};
+  size_t off = 0;
+  auto take = [&](size_t bytes) { size_t at = off; off = align_up(off + bytes, 256); return at; };
+  L.status = take(256);
+  L.counters = take((size_t)kAttnMaxCtas * 4);
+  L.parts = take(2 * (size_t)kAttnMaxCtas * kDecodeRows * a.D * 4);
+  L.ml = take(2 * (size_t)kAttnMaxCtas * kDecodeRows * 8);
+  (void)prefill;
+  L.total = off;
+  return L;
+}
+
+// ---- launchers -----------------------------------------------------------------------------
+cudaError_t launch_attn_append(const AttnDims& a, const void* q, const void* k, const void* v,
+                               const void* q_norm, const void* k_norm, const float* cos_sin,
+                               const int32_t* positions, const int32_t* block_table,
+                               const int32_t* kv_len, const int32_t* q_start,
+                               const float* k_scale, const float* v_scale, void* q_out,
+                               void* k_cache, void* v_cache, int* status, cudaStream_t st);
+cudaError_t launch_attn_decode(const AttnDims& a, const void* q, const void* k_cache,
+                               const void* v_cache, const float* k_scale, const float* v_scale,
+                               const int32_t* block_table, const int32_t* kv_len, void* o,
+                               float* lse, char* ws, const AttnWs& L, cudaStream_t st);
+
+#ifdef __CUDACC__
+__device__ __forceinline__ uint32_t div_fast(uint32_t n, const FastDiv& f) {
+  return (uint32_t)(((uint64_t)n * f.m) >> f.p);
+}
+
+// two fp32 -> packed bf16 (lo in the low half), round to nearest even
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+__device__ __forceinline__ float ex2(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+
+__device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
+#endif
+
+}  // namespace moe

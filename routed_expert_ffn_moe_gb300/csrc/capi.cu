@@ -6,14 +6,15 @@
 #include <mutex>
 #include <vector>
 
+#include "capi.h"
 #include "internal.h"
 
 namespace moe {
 
 namespace {
 thread_local char g_err[512] = "";
+}
 
-moe_status fail(moe_status st, const char* fmt, ...) __attribute__((format(printf, 2, 3)));
 moe_status fail(moe_status st, const char* fmt, ...) {
   va_list ap;
   va_start(ap, fmt);
@@ -26,8 +27,7 @@ moe_status cuda_fail(cudaError_t e, const char* where) {
   return fail(MOE_ERR_CUDA, "%s: %s", where, cudaGetErrorString(e));
 }
 
-bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
-
+namespace {
 moe_status check_shape(const moe_shape* s) {
   if (!s) return fail(MOE_ERR_INVALID_ARG, "shape is NULL");
   if (s->E < 1 || s->E > 1024) return fail(MOE_ERR_INVALID_ARG, "E=%d not in [1, 1024]", s->E);
@@ -46,13 +46,6 @@ moe_status check_shape(const moe_shape* s) {
     return fail(MOE_ERR_INVALID_ARG, "wdtype=%d unknown", s->wdtype);
   return MOE_OK;
 }
-
-#define REQUIRE_PTR(p, align)                                                          \
-  do {                                                                                  \
-    if (!(p)) return fail(MOE_ERR_INVALID_ARG, "%s is NULL", #p);                       \
-    if (!aligned((p), (align)))                                                         \
-      return fail(MOE_ERR_INVALID_ARG, "%s not %d-byte aligned", #p, (int)(align));     \
-  } while (0)
 
 // Expert weights and their scales: bf16 has none; E4M3 and MXFP4 need both. MXFP4 code arrays
 // are read through tensor maps that want 32-byte aligned bases.
