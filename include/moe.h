@@ -309,6 +309,22 @@ MOE_API moe_status moe_attn_decode(const moe_attn_shape* shape, const void* q,
                                    const int32_t* block_table, const int32_t* kv_len, void* o,
                                    float* lse, void* ws, size_t ws_bytes, void* stream);
 
+/* Attention of any number of new tokens per sequence over the cache, which holds them already:
+ * prompts, chunks of prompts over what is cached, in one ragged step.
+ *   q [T, Hq, D] bf16, o [T, Hq, D] bf16 out, lse [T, Hq] fp32 out or NULL; rows of o and lse from
+ *   q_start[B] on are not written. A token that sees no place gives o = 0 and lse = -inf.
+ * Scores, the softmax's maximum and sum and the output are held in fp32; the probabilities enter
+ * the product with v as bf16. What the cache holds at the places of a sequence must be finite
+ * (a NaN there spreads to earlier tokens of its tile; beyond kv_len and left of the window it does
+ * not). E4M3 caches, and bf16 caches whose pages are not 8, 16, 32, 64 or a multiple of 128 tokens,
+ * are first unpacked into the workspace (4 B Hkv max_pages page_size D bytes). */
+MOE_API moe_status moe_attn_prefill(const moe_attn_shape* shape, const void* q,
+                                    const void* k_cache, const void* v_cache,
+                                    const float* k_scale, const float* v_scale,
+                                    const int32_t* block_table, const int32_t* kv_len,
+                                    const int32_t* q_start, void* o, float* lse, void* ws,
+                                    size_t ws_bytes, void* stream);
+
 /* Reads (and clears) the first device-side error recorded in `ws` since the last check.
  * Synchronises `stream`. Returns MOE_OK, MOE_ERR_DEVICE_BOUNDS or MOE_ERR_DEVICE_TIMEOUT (or
  * MOE_ERR_CUDA if the read itself fails). */

@@ -19,7 +19,7 @@ __all__ = ["MoeError", "MoeShape", "MOE_W_BF16", "MOE_W_FP8_E4M3_B128", "MOE_W_M
            "moe_last_error_string", "shape_of", "MoeLayer", "EXPORTED",
            "MoeAttnShape", "MOE_KV_BF16", "MOE_KV_FP8_E4M3", "attn_shape",
            "moe_attn_workspace_size", "moe_attn_workspace_zero_bytes", "moe_attn_append",
-           "moe_attn_decode"]
+           "moe_attn_decode", "moe_attn_prefill"]
 
 MOE_W_BF16, MOE_W_FP8_E4M3_B128, MOE_W_MXFP4_E8M0_B32 = 0, 1, 2
 WDTYPES = {"bf16": MOE_W_BF16, "fp8": MOE_W_FP8_E4M3_B128, "mxfp4": MOE_W_MXFP4_E8M0_B32}
@@ -34,7 +34,7 @@ EXPORTED = ("moe_workspace_size", "moe_route", "moe_route_hash", "moe_route_noal
             "moe_check_device_status", "moe_selftest_bounded_wait", "moe_profile_enable",
             "moe_profile_read", "moe_last_error_string",
             "moe_attn_workspace_size", "moe_attn_workspace_zero_bytes", "moe_attn_append",
-            "moe_attn_decode")
+            "moe_attn_decode", "moe_attn_prefill")
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 
@@ -114,6 +114,8 @@ def load():
     L.moe_attn_append.argtypes = [ashp] + [vp] * 16 + [sz, vp]
     L.moe_attn_decode.restype = i32
     L.moe_attn_decode.argtypes = [ashp] + [vp] * 10 + [sz, vp]
+    L.moe_attn_prefill.restype = i32
+    L.moe_attn_prefill.argtypes = [ashp] + [vp] * 11 + [sz, vp]
     L.moe_last_error_string.restype = ctypes.c_char_p
     L.moe_last_error_string.argtypes = []
     _lib = L
@@ -287,6 +289,17 @@ def moe_attn_decode(shape, q, k_cache, v_cache, k_scale, v_scale, block_table, k
                                   _ptr(k_scale), _ptr(v_scale), _ptr(block_table), _ptr(kv_len),
                                   _ptr(o), _ptr(lse), wp, wb if ws_bytes is None else ws_bytes,
                                   _stream(stream)), "moe_attn_decode")
+
+
+def moe_attn_prefill(shape, q, k_cache, v_cache, k_scale, v_scale, block_table, kv_len, q_start,
+                     o, lse, ws, stream=None, ws_bytes=None):
+    """Attention of a ragged step of new tokens over the paged cache (which holds them already)."""
+    wp, wb = _ws(ws)
+    _check(load().moe_attn_prefill(ctypes.byref(shape), _ptr(q), _ptr(k_cache), _ptr(v_cache),
+                                   _ptr(k_scale), _ptr(v_scale), _ptr(block_table), _ptr(kv_len),
+                                   _ptr(q_start), _ptr(o), _ptr(lse), wp,
+                                   wb if ws_bytes is None else ws_bytes, _stream(stream)),
+           "moe_attn_prefill")
 
 
 class MoeLayer:

@@ -36,13 +36,30 @@ struct AttnDims {
 //                                     them at zero
 //   parts     f32 [2 * ctas][16][D]   decode: unnormalised outputs of split items
 //   ml        f32 [2 * ctas][16][2]   decode: their running maxima and sums
+//   unpacked  bf16 [2][B][Hkv][Lp][D] prefill over a cache that its tiles cannot read as it lies:
+//                                     keys, then values, each sequence in a row; Lp is
+//                                     max_pages * page_size rounded up to a tile
 constexpr int kAttnMaxCtas = 2048;
 constexpr size_t kAttnZeroBytes = 256 + (size_t)kAttnMaxCtas * 4;
 constexpr int kDecodeRows = 16;  // query heads of one decode item
 
 struct AttnWs {
-  size_t status, counters, parts, ml, total;
+  size_t status, counters, parts, ml, unpacked, total;
 };
+
+constexpr int kPrefillKeys = 128;  // keys of a prefill tile
+
+// Prefill tiles are read by TMA, a page (or a tile's part of one) a box of whole 8-row swizzle
+// atoms: bf16 pages of 8, 16, 32, 64 or a multiple of 128 tokens. Other caches are unpacked first.
+inline bool prefill_reads_pages(const AttnDims& a) {
+  const int p = a.page_size;
+  return !a.fp8 && (p % kPrefillKeys == 0 || p == 8 || p == 16 || p == 32 || p == 64);
+}
+
+inline int64_t unpacked_len(const AttnDims& a) {
+  const int64_t n = (int64_t)a.max_pages * a.page_size;
+  return (n + kPrefillKeys - 1) / kPrefillKeys * kPrefillKeys;
+}
 
 inline AttnWs attn_ws(const AttnDims& a, int prefill) {
   AttnWs L{};
@@ -52,7 +69,8 @@ inline AttnWs attn_ws(const AttnDims& a, int prefill) {
   L.counters = take((size_t)kAttnMaxCtas * 4);
   L.parts = take(2 * (size_t)kAttnMaxCtas * kDecodeRows * a.D * 4);
   L.ml = take(2 * (size_t)kAttnMaxCtas * kDecodeRows * 8);
-  (void)prefill;
+  const bool unpack = prefill && !prefill_reads_pages(a);
+  L.unpacked = take(unpack ? 4 * (size_t)a.B * a.Hkv * unpacked_len(a) * a.D : 0);
   L.total = off;
   return L;
 }
@@ -68,6 +86,12 @@ cudaError_t launch_attn_decode(const AttnDims& a, const void* q, const void* k_c
                                const void* v_cache, const float* k_scale, const float* v_scale,
                                const int32_t* block_table, const int32_t* kv_len, void* o,
                                float* lse, char* ws, const AttnWs& L, cudaStream_t st);
+
+cudaError_t launch_attn_prefill(const AttnDims& a, const void* q, const void* k_cache,
+                                const void* v_cache, const float* k_scale, const float* v_scale,
+                                const int32_t* block_table, const int32_t* kv_len,
+                                const int32_t* q_start, void* o, float* lse, char* ws,
+                                const AttnWs& L, cudaStream_t st);
 
 #ifdef __CUDACC__
 __device__ __forceinline__ uint32_t div_fast(uint32_t n, const FastDiv& f) {

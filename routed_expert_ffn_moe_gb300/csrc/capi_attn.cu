@@ -181,4 +181,32 @@ moe_status moe_attn_decode(const moe_attn_shape* shape, const void* q, const voi
   return e == cudaSuccess ? MOE_OK : cuda_fail(e, "moe_attn_decode launch");
 }
 
+moe_status moe_attn_prefill(const moe_attn_shape* shape, const void* q, const void* k_cache,
+                            const void* v_cache, const float* k_scale, const float* v_scale,
+                            const int32_t* block_table, const int32_t* kv_len,
+                            const int32_t* q_start, void* o, float* lse, void* ws,
+                            size_t ws_bytes, void* stream) {
+  AttnDims a;
+  moe_status st = check_attn(shape, &a);
+  if (st != MOE_OK) return st;
+  if ((int64_t)a.T * a.Hkv >= (int64_t)1 << 31)
+    return fail(MOE_ERR_INVALID_ARG, "T=%d times Hkv=%d is over 2^31", a.T, a.Hkv);
+  AttnWs L;
+  if ((st = check_attn_ws(a, 1, ws, ws_bytes, &L)) != MOE_OK) return st;
+  if (a.T == 0 || a.B == 0) return MOE_OK;
+  REQUIRE_PTR(q, 16);
+  REQUIRE_PTR(k_cache, 16);
+  REQUIRE_PTR(v_cache, 16);
+  REQUIRE_PTR(block_table, 4);
+  REQUIRE_PTR(kv_len, 4);
+  REQUIRE_PTR(q_start, 4);
+  REQUIRE_PTR(o, 16);
+  if (!aligned(lse, 4)) return fail(MOE_ERR_INVALID_ARG, "lse not 4-byte aligned");
+  if ((st = check_scales(a, k_scale, v_scale)) != MOE_OK) return st;
+  cudaError_t e = launch_attn_prefill(a, q, k_cache, v_cache, k_scale, v_scale, block_table,
+                                      kv_len, q_start, o, lse, static_cast<char*>(ws), L,
+                                      static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? MOE_OK : cuda_fail(e, "moe_attn_prefill launch");
+}
+
 }  // extern "C"

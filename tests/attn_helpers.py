@@ -122,7 +122,7 @@ class Step:
             out.append(x if sc is None else x * sc.to(F64)[:, None])
         return out
 
-    def reference(self):
+    def reference(self, p_round=2.0 ** -9):
         """o, lse in 64 bits and their bounds: see attention_bounds."""
         o = torch.zeros(self.T, self.Hq, self.D, dtype=F64)
         lse = torch.full((self.T, self.Hq), -math.inf, dtype=F64)
@@ -145,7 +145,7 @@ class Step:
                 p = torch.exp(s - L[..., None]).nan_to_num(0.0)
                 y = torch.einsum("thgj,jhd->thgd", p, v)
                 yabs = torch.einsum("thgj,jhd->thgd", p, v.abs())
-                e_o, e_l = attention_bounds(y, yabs, big, n, L)
+                e_o, e_l = attention_bounds(y, yabs, big, n, L, p_round)
                 for dst, src in ((o, y), (o_tol, e_o)):
                     dst[t0:t0 + new] = torch.where(some[:, None, None], src.reshape(new, self.Hq, self.D), 0.0)
                 lse[t0:t0 + new] = L.reshape(new, self.Hq)
@@ -154,18 +154,18 @@ class Step:
         return o, lse, o_tol, lse_tol
 
 
-def attention_bounds(y, yabs, big, n, lse):
+def attention_bounds(y, yabs, big, n, lse, p_round=2.0 ** -9):
     """Bounds of |o - y| and |lse error| for an output y = sum p v.
 
     A score is a sum of D <= 128 exact products in fp32: within 128 * 2^-24 of the sum of their
     magnitudes (`big`: the largest over the keys, scale included), and its scaling adds 2^-22 of it.
     Each e^s carries that and 2^-21 of its own (base-2 exponential and its argument); a
-    probability enters the product rounded to bf16 (2^-9 relative, l is summed before the rounding),
-    so numerator and l together move y by at most (2^-9 + 2 e) sum p |v|. fp32 sums over n keys
+    probability enters the product within `p_round` of itself (l is summed before that rounding),
+    so numerator and l together move y by at most (p_round + 2 e) sum p |v|. fp32 sums over n keys
     (at most n/8 + 64 in a row) add their own, and the result is rounded to bf16."""
     e = big * (2.0 ** -17 + 2.0 ** -22) + 2.0 ** -21
     sums = (n / 8 + 64) * 2.0 ** -24
-    o_tol = half_ulp_bf16(y) * 1.01 + (2.0 ** -9 + 2 * e + 2 * sums)[..., None] * yabs + 1e-30
+    o_tol = half_ulp_bf16(y) * 1.01 + (p_round + 2 * e + 2 * sums)[..., None] * yabs + 1e-30
     lse_tol = e + sums + lse.abs() * 2.0 ** -22
     return o_tol, lse_tol.nan_to_num(0.0)
 
@@ -177,8 +177,8 @@ def workspace(shape, prefill=False):
     return ws
 
 
-def check_attention(step, o, lse, what=""):
-    ref, ref_lse, o_tol, lse_tol = step.reference()
+def check_attention(step, o, lse, what="", p_round=2.0 ** -9):
+    ref, ref_lse, o_tol, lse_tol = step.reference(p_round)
     o, lse = o.cpu().to(F64), lse.cpu().to(F64)
     assert torch.isfinite(o).all(), (what, "o is not finite")
     over = (o - ref).abs() - o_tol

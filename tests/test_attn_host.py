@@ -121,8 +121,36 @@ def test_bad_pointers_of_decode_are_refused():
     assert "shape is NULL" in moe.moe_last_error_string()
 
 
+def test_bad_pointers_of_prefill_are_refused():
+    # q, k_cache, v_cache, k_scale, v_scale, table, kv_len, q_start, o, lse
+    good = [F, F, F, None, None, F, F, F, F, F]
+    for i, name in ((0, "q is NULL"), (1, "k_cache"), (2, "v_cache"), (5, "block_table"),
+                    (6, "kv_len"), (7, "q_start"), (8, "o is NULL")):
+        bad = list(good)
+        bad[i] = None
+        refused(moe.moe_attn_prefill, bad, name)
+    for i, name in ((0, "q not"), (8, "o not")):
+        bad = list(good)
+        bad[i] = F + 8
+        refused(moe.moe_attn_prefill, bad, name)
+    bad = list(good)
+    bad[9] = F + 2
+    refused(moe.moe_attn_prefill, bad, "lse")
+    bad = list(good)
+    bad[4] = F
+    refused(moe.moe_attn_prefill, bad, "must be NULL for a bf16 cache")
+    refused(moe.moe_attn_prefill, good, "2^31", s=shape(T=1 << 24, Hkv=1024, Hq=1024))
+    refused(moe.moe_attn_prefill, good, "D=32", code=-2, s=shape(D=32, rot_dim=0))
+    # an E4M3 cache is unpacked first: the plain workspace is too small for that
+    s = shape(kv_dtype="fp8")
+    n = moe.moe_attn_workspace_size(s)
+    assert moe.moe_attn_workspace_size(s, True) >= n + 4 * 4 * 2 * 8 * 16 * 128
+    refused(moe.moe_attn_prefill, good, "workspace", code=-3, ws_bytes=n, s=s)
+
+
 def test_empty_steps_launch_nothing():
     s = shape(T=0, B=0)
+    moe.moe_attn_prefill(s, *[None] * 10, F, stream=0, ws_bytes=WS)
     moe.moe_attn_decode(s, None, None, None, None, None, None, None, None, None, F, stream=0,
                         ws_bytes=WS)
     moe.moe_attn_append(s, *[None] * 15, F, stream=0, ws_bytes=WS)
