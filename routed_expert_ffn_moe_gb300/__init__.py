@@ -131,10 +131,22 @@ def _ptr(t):
     return t.data_ptr()
 
 
+def _current_stream():
+    """The current torch stream's handle, without the Stream object where torch offers that."""
+    global _current_stream
+    import torch
+    try:
+        raw, dev = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
+        raw(dev())
+        _current_stream = lambda: raw(dev())                            # noqa: E731
+    except AttributeError:
+        _current_stream = lambda: torch.cuda.current_stream().cuda_stream  # noqa: E731
+    return _current_stream()
+
+
 def _stream(stream):
     if stream is None:
-        import torch
-        return torch.cuda.current_stream().cuda_stream
+        return _current_stream()
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream

@@ -47,14 +47,11 @@ struct AttnWs {
   size_t status, counters, parts, ml, unpacked, total;
 };
 
-constexpr int kPrefillKeys = 128;  // keys of a prefill tile
+constexpr int kPrefillKeys = 128;  // the unpacked rows are made in runs of so many places
 
-// Prefill tiles are read by TMA, a page (or a tile's part of one) a box of whole 8-row swizzle
-// atoms: bf16 pages of 8, 16, 32, 64 or a multiple of 128 tokens. Other caches are unpacked first.
-inline bool prefill_reads_pages(const AttnDims& a) {
-  const int p = a.page_size;
-  return !a.fp8 && (p % kPrefillKeys == 0 || p == 8 || p == 16 || p == 32 || p == 64);
-}
+// Prefill tiles are read by TMA, whole 8-row swizzle atoms of a page at a time: bf16 pages of a
+// multiple of 8 tokens. Other caches are unpacked first.
+inline bool prefill_reads_pages(const AttnDims& a) { return !a.fp8 && a.page_size % 8 == 0; }
 
 inline int64_t unpacked_len(const AttnDims& a) {
   const int64_t n = (int64_t)a.max_pages * a.page_size;

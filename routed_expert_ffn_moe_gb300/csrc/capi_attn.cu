@@ -189,8 +189,8 @@ moe_status moe_attn_prefill(const moe_attn_shape* shape, const void* q, const vo
   AttnDims a;
   moe_status st = check_attn(shape, &a);
   if (st != MOE_OK) return st;
-  if ((int64_t)a.T * a.Hkv >= (int64_t)1 << 31)
-    return fail(MOE_ERR_INVALID_ARG, "T=%d times Hkv=%d is over 2^31", a.T, a.Hkv);
+  if ((int64_t)a.T * a.Hkv >= (int64_t)1 << 30)
+    return fail(MOE_ERR_INVALID_ARG, "T=%d times Hkv=%d is over 2^30", a.T, a.Hkv);
   AttnWs L;
   if ((st = check_attn_ws(a, 1, ws, ws_bytes, &L)) != MOE_OK) return st;
   if (a.T == 0 || a.B == 0) return MOE_OK;

@@ -139,7 +139,7 @@ def test_bad_pointers_of_prefill_are_refused():
     bad = list(good)
     bad[4] = F
     refused(moe.moe_attn_prefill, bad, "must be NULL for a bf16 cache")
-    refused(moe.moe_attn_prefill, good, "2^31", s=shape(T=1 << 24, Hkv=1024, Hq=1024))
+    refused(moe.moe_attn_prefill, good, "2^30", s=shape(T=1 << 24, Hkv=1024, Hq=1024))
     refused(moe.moe_attn_prefill, good, "D=32", code=-2, s=shape(D=32, rot_dim=0))
     # an E4M3 cache is unpacked first: the plain workspace is too small for that
     s = shape(kv_dtype="fp8")
