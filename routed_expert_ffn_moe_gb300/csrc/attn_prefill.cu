@@ -38,6 +38,8 @@
 // What the cache holds beyond kv_len never enters a product: pages there are not read (TMA fills
 // zeros for coordinates beyond the map), and the rest of the last page is zeroed in shared
 // memory, since 0 * NaN in P V would not vanish.
+#include <type_traits>
+
 #include "attn.h"
 #include "tc_common.cuh"
 
@@ -300,23 +302,18 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (w.n > 0 && (warp == 8 || warp == 10)) {
       // ---------------- TMA: warp 8 Q and K, warp 10 V (one thread each) ----------------
       const int kv = warp == 8 ? 0 : 1;
-      uint8_t* ring_kv = ring + kv * (C::kSlots * C::kSlot);
+      const uint32_t ring_kv = smem_u32(ring) + kv * (C::kSlots * C::kSlot);
       if (elect_one()) {
-        const uint64_t pol = policy_evict_normal();
         if (kv == 0) {
           const uint32_t bytes = C::kHalves * (uint32_t)(p.G * p.TQ) * 128;
-          const uint32_t q_bar = PAIR ? mapa_shared(smem_u32(&q_full[0]), 0) : 0;
           for (int i = 0; i < 2; ++i) {
             if (i * span >= w.ntok) break;
             if (rank == 0) mbar_arrive_expect_tx(&q_full[i], C::kBlocks * bytes);
-            for (int hf = 0; hf < C::kHalves; ++hf) {
-              void* dst = q_s + i * C::kQTile + hf * C::kHalfBytes;
-              const int tok = w.tok0 + i * span + rank * p.TQ;
-              if (PAIR)
-                tma_load_3d_pair(dst, &tm_q, q_bar + 8 * i, hf * 64, w.h * p.G, tok, pol);
-              else
-                tma_load_3d(dst, &tm_q, &q_full[i], hf * 64, w.h * p.G, tok, pol);
-            }
+            const uint32_t bar =
+                PAIR ? mapa_shared(smem_u32(&q_full[i]), 0) : smem_u32(&q_full[i]);
+            for (int hf = 0; hf < C::kHalves; ++hf)
+              tma_load_3d<PAIR>(smem_u32(q_s) + i * C::kQTile + hf * C::kHalfBytes, &tm_q, bar,
+                                hf * 64, w.h * p.G, w.tok0 + i * span + rank * p.TQ);
           }
         }
         // A tile's boxes: rows box * rows .. of this block's part. K of a pair: its 32 places, both
@@ -324,71 +321,71 @@ __global__ void __launch_bounds__(kThreads, 1)
         // places of its half; else all 64 places.
         constexpr int kKRows = kKeys / C::kHalves;
         const int rows = kv ? p.v_rows : p.k_rows;
+        const int part = kv ? kKeys : kKRows;                 // places of the block's part
         const bool split = kv == 0 && PAIR && rows < kKRows;  // halves in boxes of their own
-        const int boxes = (kv ? kKeys : kKRows) / rows * (split ? 2 : 1);
-        const int first = kv ? 0 : rank * kKRows;             // this block's first place of a tile
+        const int first = kv ? 0 : rank * kKRows;             // its first place of a tile
+        const int half = kv && PAIR ? rank : 0;
         const int end = min(w.len, w.pos0 + w.ntok);          // places any row sees
         const int lo = p.window ? max(0, w.pos0 - p.window + 1) : 0;
         const int32_t* table = p.block_table + (int64_t)w.b * p.max_pages;
         const CUtensorMap* map = kv ? &tm_v : &tm_k;
-        const uint32_t full_bar = PAIR ? mapa_shared(smem_u32(&full[kv][0]), 0) : 0;
-        // the pages that a tile's boxes lie in, looked up a step before they are used, and which of
-        // the boxes any row sees
-        int page[kKeys / 8];
-        uint32_t seen = 0;
-        const auto look_up = [&](int j) {
-          seen = 0;
-#pragma unroll
-          for (int b = 0; b < kKeys / 8; ++b) {
-            if (b >= boxes) break;
-            const int key = key_tile(w, j) * kKeys + first + (split ? b >> 1 : b) * rows;
-            if (key < end && (key + rows > lo || key < p.n_sink)) {
-              seen |= 1u << b;
-              page[b] = p.block_table ? __ldg(table + div_fast((uint32_t)key, p.page_div)) : w.b;
+        const uint32_t full_bar = PAIR ? mapa_shared(smem_u32(&full[kv][0]), 0)
+                                       : smem_u32(&full[kv][0]);
+        // page and row of the box at place `key`; the page is beyond the map, which reads as zeros,
+        // if no row sees the box
+        const auto look_up = [&](int key, int& page, int& row) {
+          page = p.num_pages;
+          row = 0;
+          if (key >= end || (key + rows <= lo && key >= p.n_sink)) return;
+          const int pg = p.block_table ? (int)div_fast((uint32_t)key, p.page_div) : w.b;
+          row = p.block_table ? key - pg * p.page_size : key;
+          page = pg;
+          if (p.block_table) {
+            page = __ldg(table + pg);
+            if ((uint32_t)page >= (uint32_t)p.num_pages) {
+              record_error(p.status, MOE_ERR_DEVICE_BOUNDS);
+              page = p.num_pages;
             }
           }
         };
-        look_up(0);
+        // the boxes of tile j into a slot, completing on `bar`; the first one's page is known
+        const auto load = [&](int j, uint32_t dst, uint32_t bar, int page, int row, auto pair) {
+          constexpr bool P = decltype(pair)::value;
+          tma_load_5d<P>(dst, map, bar, 0, row, half, w.h, page);
+          if (split) tma_load_5d<P>(dst + C::kKHalf, map, bar, 0, row, 1, w.h, page);
+          for (int r = rows; r < part; r += rows) {
+            look_up(key_tile(w, j) * kKeys + first + r, page, row);
+            tma_load_5d<P>(dst + r * 128, map, bar, 0, row, half, w.h, page);
+            if (split) tma_load_5d<P>(dst + C::kKHalf + r * 128, map, bar, 0, row, 1, w.h, page);
+          }
+        };
+        int page, row;  // of the next tile's first box: looked up a step before they are used
+        look_up(key_tile(w, 0) * kKeys + first, page, row);
+        // the last V tile is completed in shared memory if it ends past kv_len
+        const int n = w.n - (kv == 1 && tail ? 1 : 0);
         bool ok = true;
         int slot = 0, issued = 0;
         uint32_t phase = 0;
-        for (int j = 0; j < w.n; ++j) {
+        for (; issued < n; ++issued) {
           ok = wait_bar(&empty[kv][slot], phase ^ 1u, abort_flag, p.status);
           if (!ok) break;
-          ++issued;
-          // the last V tile is completed in shared memory if it ends past kv_len
-          const bool to_tail = kv == 1 && tail && j + 1 == w.n;
-          if (to_tail) {
+          if (rank == 0) mbar_arrive_expect_tx(&full[kv][slot], C::kBlocks * C::kSlot);
+          const int pg = page, rw = row;
+          load(issued, ring_kv + slot * C::kSlot, full_bar + 8 * slot, pg, rw,
+               std::integral_constant<bool, PAIR>());
+          if (issued + 1 < w.n) look_up(key_tile(w, issued + 1) * kKeys + first, page, row);
+          if (++slot == C::kSlots) { slot = 0; phase ^= 1u; }
+        }
+        if (ok && n < w.n) {
+          ok = wait_bar(&empty[kv][slot], phase ^ 1u, abort_flag, p.status);
+          if (ok) {
             mbar_arrive_expect_tx(&tail_full, C::kSlot);
             if (rank == 0) mbar_arrive(&full[kv][slot]);
-          } else if (rank == 0) {
-            mbar_arrive_expect_tx(&full[kv][slot], C::kBlocks * C::kSlot);
+            load(n, ring_kv + slot * C::kSlot, smem_u32(&tail_full), page, row,
+                 std::integral_constant<bool, false>());
+            ++issued;
+            if (++slot == C::kSlots) { slot = 0; phase ^= 1u; }
           }
-          const int key0 = key_tile(w, j) * kKeys + first;
-#pragma unroll
-          for (int b = 0; b < kKeys / 8; ++b) {
-            if (b >= boxes) break;
-            const int r = (split ? b >> 1 : b) * rows;
-            const int half = kv ? (PAIR ? rank : 0) : (split ? b & 1 : 0);
-            int row = key0 + r;
-            if (p.block_table) row -= (int)div_fast((uint32_t)row, p.page_div) * p.page_size;
-            int pg = p.num_pages;  // beyond the map: zeros
-            if (seen >> b & 1) {
-              if ((uint32_t)page[b] < (uint32_t)p.num_pages)
-                pg = page[b];
-              else
-                record_error(p.status, MOE_ERR_DEVICE_BOUNDS);
-            }
-            uint8_t* dst = ring_kv + slot * C::kSlot + (split ? half * (int)C::kKHalf : 0) + r * 128;
-            if (to_tail)
-              tma_load_5d(dst, map, &tail_full, 0, row, half, w.h, pg, pol);
-            else if (PAIR)
-              tma_load_5d_pair(dst, map, full_bar + 8 * slot, 0, row, half, w.h, pg, pol);
-            else
-              tma_load_5d(dst, map, &full[kv][slot], 0, row, half, w.h, pg, pol);
-          }
-          if (j + 1 < w.n) look_up(j + 1);
-          if (++slot == C::kSlots) { slot = 0; phase ^= 1u; }
         }
         // every load issued has landed before the block may exit (in pairs the even block's
         // barriers count both blocks' bytes)
@@ -423,7 +420,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
     } else if (w.n > 0 && (warp == 9 || warp == 11) && rank == 0) {
-      // ---------------- MMA: warp 9 row tile 0, warp 11 row tile 1 ----------------
+      // ---------------- MMA: warp 9 row tile 0, warp 11 row tile 1 (one thread each) ----------------
       const int i = warp == 9 ? 0 : 1;
       const RowTile rt = row_tile(p, w, i * span, span);
       const uint32_t idesc_s = idesc_bf16(kRows * C::kBlocks, kKeys);
@@ -438,72 +435,72 @@ __global__ void __launch_bounds__(kThreads, 1)
         else
           mma_commit(bar);
       };
-      int n_qk = 0, n_pv = 0;  // products issued: the buffer and phase of the next
-      int ks = 0, vs = 0;      // slots of the next K and V tile
-      uint32_t kp = 0, vp = 0;
-      bool ok = rt.ntok <= 0 || wait_bar(&q_full[i], 0, abort_flag, p.status);
-      ok = __all_sync(0xffffffffu, ok);
-      for (int j = -1; ok && j < w.n; ++j) {
-        if (j + 1 < w.n) {  // S = Q K(j+1)
-          // also where the row tile sees nothing of it: its slot is not handed back unread
-          ok = wait_bar(&full[0][ks], kp, abort_flag, p.status);
-          ok = __all_sync(0xffffffffu, ok);
-          if (!ok) break;
-          const bool qk = sees(rt, j + 1);
-          tc_fence_after();
-          if (elect_one()) {
-            if (qk) {
-              const uint64_t dk = dk0 + (uint64_t)(ks * (int)(C::kSlot >> 4));
-              const uint32_t d = s_t + (n_qk & 1) * kKeys;
+      if (elect_one()) {
+        int n_qk = 0, n_pv = 0;  // products issued: the buffer and phase of the next
+        int ks = 0, vs = 0;      // slots of the next K and V tile
+        uint32_t kp = 0, vp = 0;
+        // S = Q K(j); the K tile has arrived
+        const auto qk = [&](int j) {
+          if (!sees(rt, j)) return;
+          const uint64_t dk = dk0 + (uint64_t)(ks * (int)(C::kSlot >> 4));
+          const uint32_t d = s_t + (n_qk & 1) * kKeys;
 #pragma unroll
-              for (int kk = 0; kk < D / 16; ++kk) {
-                const uint64_t qa = dq + (uint64_t)((kk >> 2) * (C::kHalfBytes >> 4) + (kk & 3) * 2);
-                const uint64_t ka = dk + (uint64_t)((kk >> 2) * (C::kKHalf >> 4) + (kk & 3) * 2);
-                if (PAIR)
-                  mma_ss_pair(d, qa, ka, idesc_s, kk ? 1u : 0u);
-                else
-                  mma_bf16_ss(d, qa, ka, idesc_s, kk ? 1u : 0u);
-              }
-              commit(&s_full[i][n_qk & 1]);
-            }
-            commit(&empty[0][ks]);
+          for (int kk = 0; kk < D / 16; ++kk) {
+            const uint64_t qa = dq + (uint64_t)((kk >> 2) * (C::kHalfBytes >> 4) + (kk & 3) * 2);
+            const uint64_t ka = dk + (uint64_t)((kk >> 2) * (C::kKHalf >> 4) + (kk & 3) * 2);
+            if (PAIR)
+              mma_ss_pair(d, qa, ka, idesc_s, kk ? 1u : 0u);
+            else
+              mma_bf16_ss(d, qa, ka, idesc_s, kk ? 1u : 0u);
           }
-          __syncwarp();
-          if (qk) ++n_qk;
+          commit(&s_full[i][n_qk & 1]);
+          ++n_qk;
+        };
+        // hands a slot back, also where the row tile saw nothing of its tile
+        const auto free_k = [&] {
+          commit(&empty[0][ks]);
           if (++ks == C::kSlots) { ks = 0; kp ^= 1u; }
+        };
+        bool ok = rt.ntok <= 0 || wait_bar(&q_full[i], 0, abort_flag, p.status);
+        for (int j = 0; ok && j < min(2, w.n); ++j) {
+          ok = wait_bar(&full[0][ks], kp, abort_flag, p.status);
+          if (!ok) break;
+          tc_fence_after();
+          qk(j);
+          free_k();
         }
-        if (j >= 0) {  // O += P V(j)
-          const bool pv = sees(rt, j);
+        for (int j = 0; ok && j < w.n; ++j) {
+          const bool more = j + 2 < w.n, pv = sees(rt, j);
+          // the operands first: once P is there, nothing else holds up the products
           ok = wait_bar(&full[1][vs], vp, abort_flag, p.status);
           if (ok && tail && j + 1 == w.n) ok = wait_bar_pair(&tail_ready, 0, abort_flag, p.status);
-          if (ok && pv)
-            ok = wait_bar(&p_full[i][n_pv & 1], (n_pv >> 1) & 1, abort_flag, p.status);
-          ok = __all_sync(0xffffffffu, ok);
+          if (ok && more) ok = wait_bar(&full[0][ks], kp, abort_flag, p.status);
+          if (ok && pv) ok = wait_bar(&p_full[i][n_pv & 1], (n_pv >> 1) & 1, abort_flag, p.status);
           if (!ok) break;
           tc_fence_after();
-          if (elect_one()) {
-            if (pv) {
-              const uint64_t dv = dv0 + (uint64_t)(vs * (int)(C::kSlot >> 4));
-              const uint32_t pa = s_t + (n_pv & 1) * kKeys;
+          if (pv) {  // O += P V(j)
+            const uint64_t dv = dv0 + (uint64_t)(vs * (int)(C::kSlot >> 4));
+            const uint32_t pa = s_t + (n_pv & 1) * kKeys;
 #pragma unroll
-              for (int kk = 0; kk < kKeys / 16; ++kk) {
-                const uint64_t at = dv + (uint64_t)(kk * (2048 >> 4));
-                const uint32_t acc = (n_pv || kk) ? 1u : 0u;
-                if (PAIR)
-                  mma_ts_pair(o_t, pa + 8 * kk, at, idesc_o, acc);
-                else
-                  mma_ts(o_t, pa + 8 * kk, at, idesc_o, acc);
-              }
-              commit(&o_full[i]);
-              if (j + 1 == rt.to) commit(&o_done[i]);
+            for (int kk = 0; kk < kKeys / 16; ++kk) {
+              const uint64_t at = dv + (uint64_t)(kk * (2048 >> 4));
+              const uint32_t acc = (n_pv || kk) ? 1u : 0u;
+              if (PAIR)
+                mma_ts_pair(o_t, pa + 8 * kk, at, idesc_o, acc);
+              else
+                mma_ts(o_t, pa + 8 * kk, at, idesc_o, acc);
             }
-            commit(&empty[1][vs]);
+            ++n_pv;
           }
-          __syncwarp();
-          if (pv) ++n_pv;
+          if (more) qk(j + 2);
+          if (pv) commit(&o_full[i]);
+          if (j + 1 == rt.to) commit(&o_done[i]);
+          commit(&empty[1][vs]);
           if (++vs == C::kSlots) { vs = 0; vp ^= 1u; }
+          if (more) free_k();
         }
       }
+      __syncwarp();
     }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
