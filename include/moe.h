@@ -269,9 +269,9 @@ typedef struct {
 
 /* Bytes of scratch for moe_attn_append and moe_attn_decode, or (prefill != 0) for
  * moe_attn_prefill as well; 0 for an invalid shape. The first moe_attn_workspace_zero_bytes()
- * bytes (the device status word and the counters that the attentions leave at zero) must be
- * zero before the first call; nothing else needs initialisation, and one workspace may serve
- * several shapes. moe_check_device_status reads its status word. */
+ * bytes (the device status word) must be zero before the first call; nothing else needs
+ * initialisation, and one workspace may serve several shapes. moe_check_device_status reads its
+ * status word. */
 MOE_API size_t moe_attn_workspace_size(const moe_attn_shape* shape, int prefill);
 MOE_API size_t moe_attn_workspace_zero_bytes(void);
 

@@ -32,19 +32,18 @@ struct AttnDims {
 
 // ---- workspace -----------------------------------------------------------------------------
 //   status    int32[64]               device error code (first error wins)
-//   counters  int32[kAttnMaxCtas]     decode: arrivals at each split item; every call leaves
-//                                     them at zero
-//   parts     f32 [2 * ctas][16][D]   decode: unnormalised outputs of split items
+//   parts     f32 [2 * ctas][16][D]   decode: unnormalised outputs of the items that span blocks,
+//                                     two a block
 //   ml        f32 [2 * ctas][16][2]   decode: their running maxima and sums
 //   unpacked  bf16 [2][B][Hkv][Lp][D] prefill over a cache that its tiles cannot read as it lies:
 //                                     keys, then values, each sequence in a row; Lp is
 //                                     max_pages * page_size rounded up to a tile
-constexpr int kAttnMaxCtas = 2048;
-constexpr size_t kAttnZeroBytes = 256 + (size_t)kAttnMaxCtas * 4;
-constexpr int kDecodeRows = 16;  // query heads of one decode item
+constexpr int kAttnMaxCtas = 512;    // blocks of a decode call, at most
+constexpr size_t kAttnZeroBytes = 256;  // the status words
+constexpr int kDecodeRows = 16;      // query heads of one decode item
 
 struct AttnWs {
-  size_t status, counters, parts, ml, unpacked, total;
+  size_t status, parts, ml, unpacked, total;
 };
 
 constexpr int kPrefillKeys = 128;  // the unpacked rows are made in runs of so many places
@@ -63,7 +62,6 @@ inline AttnWs attn_ws(const AttnDims& a, int prefill) {
   size_t off = 0;
   auto take = [&](size_t bytes) { size_t at = off; off = align_up(off + bytes, 256); return at; };
   L.status = take(256);
-  L.counters = take((size_t)kAttnMaxCtas * 4);
   L.parts = take(2 * (size_t)kAttnMaxCtas * kDecodeRows * a.D * 4);
   L.ml = take(2 * (size_t)kAttnMaxCtas * kDecodeRows * 8);
   const bool unpack = prefill && !prefill_reads_pages(a);

@@ -158,7 +158,7 @@ def test_empty_steps_launch_nothing():
 
 def test_workspace_sizes():
     n = moe.moe_attn_workspace_size(shape())
-    assert n > moe.moe_attn_workspace_zero_bytes() > 256 and n % 256 == 0
+    assert n > moe.moe_attn_workspace_zero_bytes() >= 4 and n % 256 == 0
     # it does not grow with the batch or the cache
     assert moe.moe_attn_workspace_size(shape(T=4096, B=4096, max_pages=8192)) == n
     assert ctypes.sizeof(moe.MoeAttnShape) == 14 * 4 + 2 * 4 + 8 * 8

@@ -83,7 +83,7 @@ def test_decode_splits(lens, kw):
     zero = moe.moe_attn_workspace_zero_bytes()
     first = run_decode(step, ws)
     check_attention(step, *first)
-    assert not ws[:zero].any()  # the counters are left as they were found
+    assert not ws[:zero].any()  # left as it was found
     for _ in range(3):          # and the result does not depend on which block came last
         again = run_decode(step, ws)
         assert torch.equal(first[0].view(torch.int16), again[0].view(torch.int16))
