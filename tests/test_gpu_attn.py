@@ -165,7 +165,7 @@ def append_case(lens, new, Hq, Hkv, D=128, kv="bf16", page=16, order="HND", rot=
     T, nq, nk = step.T, Hq * D, Hkv * D
     qkv = (torch.randn(T, nq + 2 * nk, generator=g) * 3).to(torch.bfloat16)
     wq = (1 + 0.2 * torch.randn(D, generator=g)).to(torch.bfloat16) if norm else None
-    wk = (1 + 0.2 * torch.randn(D, generator=g)).to(torch.bfloat16) if norm else None
+    wk = (1 + 0.2 * torch.randn(D, generator=g)).to(torch.bfloat16) if norm is True else None
     max_pos = max(max(lens), 1) + 50
     freq = 10000.0 ** (-torch.arange(rot // 2, dtype=F64) / max(rot // 2, 1))
     ang = torch.arange(max_pos, dtype=F64)[:, None] * freq
@@ -186,7 +186,7 @@ def append_case(lens, new, Hq, Hkv, D=128, kv="bf16", page=16, order="HND", rot=
     s = step.shape(rot_dim=rot, rot_pairs=pairs, max_pos=max_pos, eps=1e-5, **strides)
     ws = workspace(s)
     before = [c.clone() for c in (t["k"], t["v"])]
-    moe.moe_attn_append(s, *parts, wq.cuda() if norm else None, wk.cuda() if norm else None,
+    moe.moe_attn_append(s, *parts, wq.cuda() if norm else None, None if wk is None else wk.cuda(),
                         cs.cuda() if rot else None,
                         pos.to(torch.int32).cuda() if positions else None, t["table"], t["lens"],
                         None if null_start else t["q_start"], t["ks"], t["vs"], q_out, t["k"],
@@ -248,6 +248,13 @@ def append_case(lens, new, Hq, Hkv, D=128, kv="bf16", page=16, order="HND", rot=
     dict(lens=[2, 9], new=[5, 1], Hq=4, Hkv=2),                             # three rows of padding
     dict(lens=[3] * 700, new=[1] * 700, Hq=4, Hkv=2, D=64),                 # more than a block's
     dict(lens=[3000], new=[2900], Hq=16, Hkv=8, kv="fp8", page=128),
+    dict(lens=[30, 5], new=[30, 1], Hq=4, Hkv=4, norm="queries"),           # keys as they are
+    # steps of more head rows than the small kernel takes, every kind of rotation
+    dict(lens=[4000, 700, 3], new=[3900, 0, 3], Hq=14, Hkv=2, norm="queries"),
+    dict(lens=[3000, 2500], new=[2000, 2500], Hq=7, Hkv=7, pairs=True, rot=64, order="NHD"),
+    dict(lens=[1, 5000, 2], new=[3, 4000, 0], Hq=20, Hkv=1, kv="fp8", rot=48, page=7, order="gaps"),
+    dict(lens=[6000], new=[5555], Hq=16, Hkv=2, D=64, page=100, in_place=True),
+    dict(lens=[6000], new=[5555], Hq=16, Hkv=2, D=64, kv="fp8", rot=0, positions=True, norm=False),
 ], ids=lambda k: "-".join(f"{a}={b}" for a, b in k.items() if a not in ("lens", "new")))
 def test_append(kw):
     append_case(**kw)
