@@ -35,15 +35,20 @@ struct AttnDims {
 //   parts     f32 [2 * ctas][16][D]   decode: unnormalised outputs of the items that span blocks,
 //                                     two a block
 //   ml        f32 [2 * ctas][16][2]   decode: their running maxima and sums
+//   prefill_parts  f32 [blocks][2][2 * 128][D]   prefill: the same of the units that runs cut
+//   prefill_ml     f32 [blocks][2][2 * 128][2]
+//   prefill_cuts   [blocks]           prefill: where each run begins
 //   unpacked  bf16 [2][B][Hkv][Lp][D] prefill over a cache that its tiles cannot read as it lies:
 //                                     keys, then values, each sequence in a row; Lp is
 //                                     max_pages * page_size rounded up to a tile
 constexpr int kAttnMaxCtas = 512;    // blocks of a decode call, at most
+constexpr int kPrefillMaxCtas = 160; // blocks of a prefill call, at most
+constexpr size_t kPrefillCutBytes = 64;
 constexpr size_t kAttnZeroBytes = 256;  // the status words
 constexpr int kDecodeRows = 16;      // query heads of one decode item
 
 struct AttnWs {
-  size_t status, parts, ml, unpacked, total;
+  size_t status, parts, ml, prefill_parts, prefill_ml, prefill_cuts, unpacked, total;
 };
 
 constexpr int kPrefillKeys = 128;  // the unpacked rows are made in runs of so many places
@@ -64,6 +69,10 @@ inline AttnWs attn_ws(const AttnDims& a, int prefill) {
   L.status = take(256);
   L.parts = take(2 * (size_t)kAttnMaxCtas * kDecodeRows * a.D * 4);
   L.ml = take(2 * (size_t)kAttnMaxCtas * kDecodeRows * 8);
+  const size_t rows = prefill ? (size_t)kPrefillMaxCtas * 2 * 2 * 128 : 0;
+  L.prefill_parts = take(rows * a.D * 4);
+  L.prefill_ml = take(rows * 8);
+  L.prefill_cuts = take(prefill ? kPrefillMaxCtas * kPrefillCutBytes : 0);
   const bool unpack = prefill && !prefill_reads_pages(a);
   L.unpacked = take(unpack ? 4 * (size_t)a.B * a.Hkv * unpacked_len(a) * a.D : 0);
   L.total = off;

@@ -55,6 +55,8 @@ constexpr int kThreads = 384;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr float kNoMax = -3e38f;     // the maximum of no scores: finite, so that -inf - it is -inf
 
+struct Cut;
+
 struct PrefillParams {
   int T, B, Hq, Hkv, G, TQ;  // TQ: tokens of a block's row tile
   int page_size, max_pages, num_pages;
@@ -72,6 +74,10 @@ struct PrefillParams {
   uint16_t* o;
   float* lse;
   int* status;
+  float* parts;       // split units: unnormalised outputs, and their running maxima and sums
+  float2* part_ml;
+  Cut* cuts;   // where each run begins, for the join
+  int min_split;      // key tiles of the shortest unit that is cut
 };
 
 template <int D>
@@ -85,9 +91,10 @@ struct Cfg {
   // (pairs), or 64 places x 64 columns
   static constexpr uint32_t kSlot = kKeys * 128;
   static constexpr uint32_t kKHalf = kSlot / kHalves;       // K: bytes of a 64-column half
-  static constexpr int kSlots = 10;                         // of K, and of V
+  static constexpr int kSlots = 8;                          // of K, and of V
+  static constexpr uint32_t kStage = 32 * 128;              // a softmax warp's rows, 128 bytes of each
   static constexpr uint32_t kQBytes = 2 * kQTile;
-  static constexpr uint32_t kSmem = kQBytes + 2 * kSlots * kSlot + 1024;
+  static constexpr uint32_t kSmem = kQBytes + 2 * kSlots * kSlot + 8 * kStage + 1024;
   static constexpr uint32_t kTmemO = 256;  // columns: S of row tile 0 (two buffers), of 1; O0, O1
   static_assert(kSmem + 1024 <= 227 * 1024, "shared memory");
 };
@@ -106,37 +113,216 @@ __device__ __forceinline__ uint64_t fma_f32x2(uint64_t a, uint64_t b, uint64_t c
   asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
   return r;
 }
+__device__ __forceinline__ uint64_t mul_f32x2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
 __device__ __forceinline__ uint64_t add_f32x2(uint64_t a, uint64_t b) {
   uint64_t r;
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
   return r;
 }
 
-// The piece of work of a block, or of a pair.
+// ---- the split of the work ----------------------------------------------------------------------
+// A unit is two row tiles of one sequence and key head (in a pair, two of 256 rows): `unit_tok`
+// tokens. All units in a row (sequence, key head, tokens ascending), each weighed by the places
+// that its last token sees plus kUnitCost for its start and end, are cut into equal runs, one per
+// block (pair) of a grid that fills the SMs. A run may begin and end inside a unit, whose parts
+// k_attn_prefill_join then joins; cuts that would leave less than kMinPart key tiles on a side,
+// or that fall into a unit of less than `min_split`, move to the unit's nearer end. A cut costs about
+// 10 us in all, a tile 0.7 us: where there are units enough for every run, units of less than 48
+// tiles stay whole, else of less than 16.
+constexpr int kUnitCost = 4 * kKeys, kMinPart = 4, kSplitFew = 16, kSplitMany = 48;
+
+// n / d of non-negative numbers: a 32-bit division where both fit
+__device__ __forceinline__ int64_t div_s(int64_t n, int64_t d) {
+  return ((n | d) >> 32) == 0 ? (int64_t)((uint32_t)n / (uint32_t)d) : n / d;
+}
+
+// One sequence's new tokens.
+struct Seq {
+  int q0, nq, len;  // first row of q, new tokens, kv_len
+};
+
+__device__ __forceinline__ Seq seq_of(const PrefillParams& p, int b) {
+  Seq s;
+  s.q0 = min(max(__ldcg(p.q_start + b), 0), p.T);
+  s.nq = min(max(__ldcg(p.q_start + b + 1), s.q0), p.T) - s.q0;
+  s.len = __ldcg(p.kv_len + b);
+  return s;
+}
+
+// Weight of a sequence's first k units (of one key head): kUnitCost each, and the places up to a
+// unit's end, none before place 0 and `cap` at most.
+__device__ __forceinline__ int64_t weight(const PrefillParams& p, const Seq& s, int unit_tok,
+                                          int k) {
+  const int64_t pos0 = (int64_t)min(max(s.len, 0), p.max_len) - s.nq;
+  const int64_t cap = (int64_t)p.window + unit_tok + p.n_sink;
+  // unit j ends at pos0 + (j + 1) unit_tok: below 0 for j < a, at most cap for j < c
+  const int64_t a = pos0 < 0 ? min((int64_t)k, div_s(-pos0, unit_tok)) : 0;
+  int64_t c = k;
+  if (p.window) c = max(a, min(c, cap > pos0 ? div_s(cap - pos0, unit_tok) : 0));
+  return (int64_t)kUnitCost * k + (c - a) * pos0 + unit_tok * (c * (c + 1) - a * (a + 1)) / 2 +
+         cap * (k - c);
+}
+
+// A unit: sequence, key head, number among the sequence's units.
+struct Unit {
+  int b, h, u;
+  Seq s;
+};
+
+// A place in the row of units: a unit, and the first step in it.
+struct Cut {
+  Unit at;
+  int step;
+  int64_t x0;          // where the unit begins in the row
+  int64_t each, more;  // weight of a run; the first `more` have one more
+};
+
+// What a unit's roles need.
 struct Work {
-  int b, h;           // sequence, key head
+  int h;
   int tok0, ntok;     // first row of q, tokens (over all row tiles)
   int pos0;           // place of the first token
   int len;            // kv_len
   int sink_tiles;     // key tiles 0 .. that hold sinks
-  int lo, n;          // first tile of the window; tiles to walk, sinks that lie before lo included
+  int lo, n;          // first tile of the window; steps, sinks that lie before lo included
   int lead;           // of these, sink tiles before lo
 };
+
+__device__ __forceinline__ Work work_of(const PrefillParams& p, const Unit& t, int unit_tok) {
+  Work w;
+  const int at = t.u * unit_tok;
+  w.h = t.h;
+  w.tok0 = t.s.q0 + at;
+  w.ntok = min(unit_tok, t.s.nq - at);
+  w.len = min(max(t.s.len, 0), p.max_len);
+  w.pos0 = w.len - t.s.nq + at;
+  const int last = w.pos0 + w.ntok - 1;
+  const int end = last >= 0 ? last / kKeys + 1 : 0;  // tiles up to the last token
+  w.lo = p.window ? min(end, max(0, w.pos0 - p.window + 1) / kKeys) : 0;
+  w.sink_tiles = (p.n_sink + kKeys - 1) / kKeys;
+  w.lead = min(w.sink_tiles, w.lo);
+  w.n = w.lead + end - w.lo;
+  return w;
+}
 
 // key tile of step j
 __device__ __forceinline__ int key_tile(const Work& w, int j) {
   return j < w.lead ? j : w.lo + j - w.lead;
 }
 
-// Tokens [first, first + span) of the work: the places p0 .. p1 of the first and the last of them,
-// and the steps [0, sink) and [from, to) whose key tiles any of them sees.
+// the next unit; false past the last
+__device__ __forceinline__ bool next_unit(const PrefillParams& p, int unit_tok, Unit& t) {
+  if ((t.u + 1) * unit_tok < t.s.nq) {
+    ++t.u;
+    return true;
+  }
+  t.u = 0;
+  if (++t.h < p.Hkv) return true;
+  t.h = 0;
+  while (++t.b < p.B) {
+    t.s = seq_of(p, t.b);
+    if (t.s.nq > 0) return true;
+  }
+  return false;
+}
+
+// Where run c of `runs` begins, found by a warp.
+__device__ __forceinline__ Cut find_cut(const PrefillParams& p, int unit_tok, int c, int runs) {
+  const int lane = (int)threadIdx.x & 31;
+  const auto all_of = [&](const Seq& s) {
+    return s.nq > 0 ? weight(p, s, unit_tok, (s.nq + unit_tok - 1) / unit_tok) : 0;
+  };
+  int64_t total = 0;
+  Seq held{0, 0, 0};  // of sequence `lane`
+  for (int b = lane; b < p.B; b += 32) {
+    const Seq s = seq_of(p, b);
+    if (s.nq > 0 && (s.len < 0 || s.len > p.max_len))
+      record_error(p.status, MOE_ERR_DEVICE_BOUNDS);
+    if (b < 32) held = s;
+    total += all_of(s);
+  }
+#pragma unroll
+  for (int o = 16; o; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+  total *= p.Hkv;
+  const int64_t each = div_s(total, runs), more = total - each * runs;
+  int64_t x = c * each + min((int64_t)c, more);
+  const int64_t here = x;
+  Cut cut;
+  cut.x0 = 0;
+  cut.each = each;
+  cut.more = more;
+  cut.at.b = p.B;
+  cut.at.h = cut.at.u = cut.step = 0;
+  cut.at.s = Seq{0, 0, 0};
+  if (x >= total) return cut;
+  for (int b0 = 0; b0 < p.B; b0 += 32) {
+    Seq s = held;
+    if (b0) s = b0 + lane < p.B ? seq_of(p, b0 + lane) : Seq{0, 0, 0};
+    const int64_t mine = all_of(s) * p.Hkv;
+    int64_t incl = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t up = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += up;
+    }
+    const int64_t all = __shfl_sync(0xffffffffu, incl, 31);
+    if (x < all) {
+      const int at = __popc(__ballot_sync(0xffffffffu, incl <= x));
+      x -= __shfl_sync(0xffffffffu, incl - mine, at);
+      cut.at.b = b0 + at;
+      cut.at.s.q0 = __shfl_sync(0xffffffffu, s.q0, at);
+      cut.at.s.nq = __shfl_sync(0xffffffffu, s.nq, at);
+      cut.at.s.len = __shfl_sync(0xffffffffu, s.len, at);
+      break;
+    }
+    x -= all;
+  }
+  const int64_t of_head = all_of(cut.at.s);
+  cut.at.h = (int)div_s(x, of_head);
+  x -= cut.at.h * of_head;
+  // the last unit that begins by x, 32 probes a round
+  int lo = 0, among = (cut.at.s.nq + unit_tok - 1) / unit_tok;
+  while (among > 1) {
+    const int gap = (among + 31) / 32, k = lane * gap;
+    const bool by = k < among && weight(p, cut.at.s, unit_tok, lo + k) <= x;
+    const int last = __popc(__ballot_sync(0xffffffffu, by)) - 1;
+    lo += last * gap;
+    among = min(gap, among - last * gap);
+  }
+  cut.at.u = lo;
+  x -= weight(p, cut.at.s, unit_tok, lo);
+  cut.x0 = here - x;
+  const int n = work_of(p, cut.at, unit_tok).n;
+  int step = x <= kUnitCost ? 0 : (int)min((int64_t)n, (x - kUnitCost) / kKeys);
+  if (n < p.min_split) step = 2 * step < n ? 0 : n;
+  if (step < kMinPart) step = 0;
+  if (step > n - kMinPart && x > 0) step = n;
+  cut.step = step;
+  if (step == n && x > 0) {  // the next unit's beginning
+    cut.step = 0;
+    if (!next_unit(p, unit_tok, cut.at)) cut.at.b = p.B;
+  }
+  return cut;
+}
+
+__device__ __forceinline__ bool same_unit(const Unit& x, const Unit& y) {
+  return x.b == y.b && x.h == y.h && x.u == y.u;
+}
+
+// Tokens [first, first + span) of a unit: the places p0 .. p1 of the first and the last of them,
+// and, of the unit's steps s0 .. s1 - 1, those in [a0, a1) and [b0, b1) whose key tiles any of
+// them sees; `last` is the last of these, or -1.
 struct RowTile {
   int p0, p1, ntok;
-  int sink, from, to;
+  int a0, a1, b0, b1, last;
 };
 
 __device__ __forceinline__ RowTile row_tile(const PrefillParams& p, const Work& w, int first,
-                                            int span) {
+                                            int span, int s0, int s1) {
   RowTile r;
   r.ntok = min(span, w.ntok - first);
   r.p0 = w.pos0 + first;
@@ -144,15 +330,19 @@ __device__ __forceinline__ RowTile row_tile(const PrefillParams& p, const Work& 
   const bool any = r.ntok > 0 && r.p1 >= 0;
   const int lo = p.window ? max(0, r.p0 - p.window + 1) / kKeys : 0;
   const int skip = w.lo - w.lead;  // tiles between the sinks' and the window's
-  r.to = any ? r.p1 / kKeys + 1 - skip : 0;
+  const int to = any ? r.p1 / kKeys + 1 - skip : 0;
   // sink tiles past the window's first are among its steps
-  r.sink = min(r.to, w.sink_tiles > w.lo ? w.sink_tiles - skip : w.lead);
-  r.from = min(r.to, max(r.sink, lo - skip));
+  const int sink = min(to, w.sink_tiles > w.lo ? w.sink_tiles - skip : w.lead);
+  r.a0 = s0;
+  r.a1 = max(s0, min(sink, s1));
+  r.b0 = max(r.a1, max(lo - skip, s0));
+  r.b1 = max(r.b0, min(to, s1));
+  r.last = r.b1 > r.b0 ? r.b1 - 1 : r.a1 > r.a0 ? r.a1 - 1 : -1;
   return r;
 }
 
 __device__ __forceinline__ bool sees(const RowTile& r, int j) {
-  return j < r.sink || (j >= r.from && j < r.to);
+  return (j >= r.a0 && j < r.a1) || (j >= r.b0 && j < r.b1);
 }
 
 // Bounded wait on an mbarrier phase: false (after recording a timeout) if it gave up or another
@@ -170,6 +360,17 @@ __device__ __forceinline__ bool wait_bar_pair(uint64_t* bar, uint32_t parity,
   return wait_bar(bar, parity, abort_flag, status) && mbar_try_wait_cluster(bar, parity);
 }
 
+// a mask of the columns 0 .. n - 1 of a tile
+__device__ __forceinline__ uint64_t below(int n) {
+  return n <= 0 ? 0 : n >= 64 ? ~0ull : (1ull << n) - 1;
+}
+
+// Row of the workspace's parts where row 0 of part `which` of run c lies: row tile i of block `rank`.
+template <class C>
+__device__ __forceinline__ int64_t part_row(int c, int which, int i, int rank) {
+  return ((((int64_t)c * 2 + which) * C::kBlocks + rank) * 2 + i) * kRows;
+}
+
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
     k_attn_prefill(const __grid_constant__ CUtensorMap tm_q,
@@ -182,32 +383,36 @@ __global__ void __launch_bounds__(kThreads, 1)
                                              ~uintptr_t(1023));
   uint8_t* q_s = smem;
   uint8_t* ring = smem + C::kQBytes;
-  // q_full, full, p_full and tail_ready are waited on in the pair's even block
-  __shared__ uint64_t q_full[2], s_full[2][2], p_full[2][2], o_full[2], o_done[2], tail_full,
-      tail_ready, full[2][C::kSlots], empty[2][C::kSlots];  // of K, of V
+  uint8_t* stage = ring + 2 * C::kSlots * C::kSlot;
+  // Phases: q_full, q_empty once a unit; tail_full once a unit that has a tail; o_done, o_free once a
+  // unit of which the row tile sees anything; the others once a tile.
+  // q_full, full, p_full and o_free are waited on in the pair's even block.
+  __shared__ uint64_t q_full, q_empty, s_full[2][2], p_full[2][2], o_full[2], o_done[2], o_free[2],
+      tail_full, full[2][C::kSlots], empty[2][C::kSlots];  // of K, of V
   __shared__ uint32_t tmem_holder;
   __shared__ int abort_flag_s;
-  __shared__ Work work_s;
+  __shared__ Cut cut_s[2];
   volatile int* abort_flag = &abort_flag_s;
   const int warp = (int)threadIdx.x >> 5, lane = (int)threadIdx.x & 31;
   const int rank = PAIR ? (int)cluster_ctarank() : 0;
 
   if (threadIdx.x == 0) {
+    mbar_init(&q_full, 1);
+    mbar_init(&q_empty, 2);                           // both row tiles' MMAs have read it
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&q_full[i], 1);
       mbar_init(&o_full[i], 1);                       // a phase for every PV
       mbar_init(&o_done[i], 1);                       // the last one
+      mbar_init(&o_free[i], 4 * C::kBlocks);          // the row tile's warps
       for (int b = 0; b < 2; ++b) {
         mbar_init(&s_full[i][b], 1);
-        mbar_init(&p_full[i][b], 4 * C::kBlocks);     // the row tile's warps
+        mbar_init(&p_full[i][b], 4 * C::kBlocks);
       }
     }
     mbar_init(&tail_full, 1);
-    mbar_init(&tail_ready, C::kBlocks);
     for (int s = 0; s < C::kSlots; ++s) {
       for (int kv = 0; kv < 2; ++kv) {
-        mbar_init(&full[kv][s], 1);
-        mbar_init(&empty[kv][s], 2);  // both row tiles' MMAs have read it
+        mbar_init(&full[kv][s], kv ? C::kBlocks : 1);  // V: every block, for the tails' sake
+        mbar_init(&empty[kv][s], 2);                  // both row tiles' MMAs have read it
       }
     }
     abort_flag_s = 0;
@@ -227,64 +432,15 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   pdl_wait_then_release();
 
-  // ---- which sequence and which of its row tiles ----
-  const int span = p.TQ * C::kBlocks;  // tokens of a row tile of the work
-  if (warp == 8) {
-    const int unit_tok = 2 * span;
-    const int unit = (int)blockIdx.x / C::kBlocks;
-    int total = 0;  // units of all sequences
-    const auto units_of = [&](int b, int& q0, int& n) {
-      q0 = min(max(__ldg(p.q_start + b), 0), p.T);
-      n = min(max(__ldg(p.q_start + b + 1), q0), p.T) - q0;
-      return (n + unit_tok - 1) / unit_tok;
-    };
-    int q0, n;
-    for (int b = lane; b < p.B; b += 32) total += units_of(b, q0, n);
-#pragma unroll
-    for (int o = 16; o; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
-    // the last units of a sequence see the most keys: they start first
-    const int want = total - 1 - unit / p.Hkv;
-    Work w{};
-    w.b = -1;
-    int before = 0;
-    for (int b0 = 0; want >= 0 && b0 < p.B; b0 += 32) {
-      const int b = b0 + lane;
-      const int mine = b < p.B ? units_of(b, q0, n) : 0;
-      int incl = mine;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int up = __shfl_up_sync(0xffffffffu, incl, o);
-        if (lane >= o) incl += up;
-      }
-      const int all = __shfl_sync(0xffffffffu, incl, 31);
-      if (want < before + all) {
-        if (before + incl > want && before + incl - mine <= want) {
-          const int at = (want - (before + incl - mine)) * unit_tok;
-          w.b = b;
-          w.h = unit % p.Hkv;
-          w.tok0 = q0 + at;
-          w.ntok = min(unit_tok, n - at);
-          int len = __ldg(p.kv_len + b);
-          if (len < 0 || len > p.max_len) record_error(p.status, MOE_ERR_DEVICE_BOUNDS);
-          len = min(max(len, 0), p.max_len);
-          w.len = len;
-          w.pos0 = len - n + at;
-          const int last = w.pos0 + w.ntok - 1;
-          const int end = last >= 0 ? last / kKeys + 1 : 0;  // tiles up to the last token
-          w.lo = p.window ? min(end, max(0, w.pos0 - p.window + 1) / kKeys) : 0;
-          w.sink_tiles = (p.n_sink + kKeys - 1) / kKeys;
-          w.lead = min(w.sink_tiles, w.lo);
-          w.n = w.lead + end - w.lo;
-          work_s = w;
-        }
-        break;
-      }
-      before += all;
-    }
-    const unsigned found = __ballot_sync(0xffffffffu, w.b >= 0);
-    if (!found && lane == 0) {
-      w.n = -1;
-      work_s = w;
+  // ---- this run: from the first cut to the second ----
+  const int span = p.TQ * C::kBlocks;  // tokens of a row tile of the unit
+  const int unit_tok = 2 * span;
+  const int run = (int)blockIdx.x / C::kBlocks, runs = (int)gridDim.x / C::kBlocks;
+  if (warp == 8 || warp == 10) {
+    const Cut c = find_cut(p, unit_tok, run + (warp == 10), runs);
+    if (lane == 0) {
+      cut_s[warp == 10] = c;
+      if (p.cuts && warp == 8 && rank == 0) p.cuts[run] = c;
     }
   }
   tc_fence_before();
@@ -292,137 +448,180 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (PAIR) cluster_sync();  // both blocks' barriers are initialised
   tc_fence_after();
   const uint32_t tmem = tmem_holder;
-  const Work w = work_s;
-  // places past kv_len share the last tile (of a cache read in place) with some before it
-  const bool tail = w.n > 0 && p.block_table && (key_tile(w, w.n - 1) + 1) * kKeys > w.len;
+  const Cut stop = cut_s[1];
+  // the run's parts: a unit and its steps [s0, s1) at a time
+  struct Part {
+    Unit t;
+    Work w;
+    int s0, s1;
+    bool tail;  // places past kv_len share the last tile (of a cache read in place) with earlier ones
+  };
+  const auto fill = [&](Part& x, int s0) {
+    x.w = work_of(p, x.t, unit_tok);
+    x.s0 = s0;
+    x.s1 = same_unit(x.t, stop.at) ? stop.step : x.w.n;
+    x.tail = p.block_table && x.s1 > s0 && x.s1 == x.w.n &&
+             (key_tile(x.w, x.w.n - 1) + 1) * kKeys > x.w.len;
+  };
+  const auto first_part = [&](Part& x) {
+    x.t = cut_s[0].at;
+    if (x.t.b >= p.B || (same_unit(x.t, stop.at) && stop.step <= cut_s[0].step)) return false;
+    fill(x, cut_s[0].step);
+    return true;
+  };
+  const auto next_part = [&](Part& x) {
+    if (same_unit(x.t, stop.at) || !next_unit(p, unit_tok, x.t)) return false;
+    if (same_unit(x.t, stop.at) && stop.step == 0) return false;
+    fill(x, 0);
+    return true;
+  };
 
   // Registers: 384 threads of 168 at launch = 128 * (200 + 200 + 104).
   if (warp >= 8) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
-    if (w.n > 0 && (warp == 8 || warp == 10)) {
+    if (warp == 8 || warp == 10) {
       // ---------------- TMA: warp 8 Q and K, warp 10 V (one thread each) ----------------
       const int kv = warp == 8 ? 0 : 1;
       const uint32_t ring_kv = smem_u32(ring) + kv * (C::kSlots * C::kSlot);
-      if (elect_one()) {
-        if (kv == 0) {
-          const uint32_t bytes = C::kHalves * (uint32_t)(p.G * p.TQ) * 128;
-          for (int i = 0; i < 2; ++i) {
-            if (i * span >= w.ntok) break;
-            if (rank == 0) mbar_arrive_expect_tx(&q_full[i], C::kBlocks * bytes);
-            const uint32_t bar =
-                PAIR ? mapa_shared(smem_u32(&q_full[i]), 0) : smem_u32(&q_full[i]);
-            for (int hf = 0; hf < C::kHalves; ++hf)
-              tma_load_3d<PAIR>(smem_u32(q_s) + i * C::kQTile + hf * C::kHalfBytes, &tm_q, bar,
-                                hf * 64, w.h * p.G, w.tok0 + i * span + rank * p.TQ);
-          }
-        }
-        // A tile's boxes: rows box * rows .. of this block's part. K of a pair: its 32 places, both
-        // 64-column halves (in one box if that takes all 32, else box by box); V of a pair: all 64
-        // places of its half; else all 64 places.
-        constexpr int kKRows = kKeys / C::kHalves;
-        const int rows = kv ? p.v_rows : p.k_rows;
-        const int part = kv ? kKeys : kKRows;                 // places of the block's part
-        const bool split = kv == 0 && PAIR && rows < kKRows;  // halves in boxes of their own
-        const int first = kv ? 0 : rank * kKRows;             // its first place of a tile
-        const int half = kv && PAIR ? rank : 0;
-        const int end = min(w.len, w.pos0 + w.ntok);          // places any row sees
-        const int lo = p.window ? max(0, w.pos0 - p.window + 1) : 0;
-        const int32_t* table = p.block_table + (int64_t)w.b * p.max_pages;
-        const CUtensorMap* map = kv ? &tm_v : &tm_k;
-        const uint32_t full_bar = PAIR ? mapa_shared(smem_u32(&full[kv][0]), 0)
-                                       : smem_u32(&full[kv][0]);
-        // page and row of the box at place `key`; the page is beyond the map, which reads as zeros,
-        // if no row sees the box
-        const auto look_up = [&](int key, int& page, int& row) {
-          page = p.num_pages;
-          row = 0;
-          if (key >= end || (key + rows <= lo && key >= p.n_sink)) return;
-          const int pg = p.block_table ? (int)div_fast((uint32_t)key, p.page_div) : w.b;
-          row = p.block_table ? key - pg * p.page_size : key;
-          page = pg;
-          if (p.block_table) {
-            page = __ldg(table + pg);
-            if ((uint32_t)page >= (uint32_t)p.num_pages) {
-              record_error(p.status, MOE_ERR_DEVICE_BOUNDS);
-              page = p.num_pages;
+      // A tile's boxes: rows box * rows .. of this block's part. K of a pair: its 32 places, both
+      // 64-column halves (in one box if that takes all 32, else box by box); V of a pair: all 64
+      // places of its half; else all 64 places.
+      constexpr int kKRows = kKeys / C::kHalves;
+      const int rows = kv ? p.v_rows : p.k_rows;
+      const int part = kv ? kKeys : kKRows;                 // places of the block's part
+      const bool split = kv == 0 && PAIR && rows < kKRows;  // halves in boxes of their own
+      const int first = kv ? 0 : rank * kKRows;             // its first place of a tile
+      const int half = kv && PAIR ? rank : 0;
+      const CUtensorMap* map = kv ? &tm_v : &tm_k;
+      const uint32_t full_bar =
+          PAIR ? mapa_shared(smem_u32(&full[kv][0]), 0) : smem_u32(&full[kv][0]);
+      int slot = 0;
+      uint32_t phase = 0, units = 0, tails = 0;
+      int64_t issued = 0;
+      bool ok = true;
+      Part x;
+      for (bool more = first_part(x); more; more = next_part(x)) {
+        const Work& w = x.w;
+        if (elect_one()) {
+          if (kv == 0) {
+            const uint32_t bytes = C::kHalves * (uint32_t)(p.G * p.TQ) * 128;
+            ok = wait_bar(&q_empty, (units & 1) ^ 1u, abort_flag, p.status);
+            if (ok) {
+              const int tiles = w.ntok > span ? 2 : 1;
+              if (rank == 0) mbar_arrive_expect_tx(&q_full, C::kBlocks * tiles * bytes);
+              const uint32_t bar = PAIR ? mapa_shared(smem_u32(&q_full), 0) : smem_u32(&q_full);
+              for (int i = 0; i < tiles; ++i)
+                for (int hf = 0; hf < C::kHalves; ++hf)
+                  tma_load_3d<PAIR>(smem_u32(q_s) + i * C::kQTile + hf * C::kHalfBytes, &tm_q, bar,
+                                    hf * 64, w.h * p.G, w.tok0 + i * span + rank * p.TQ);
             }
           }
-        };
-        // the boxes of tile j into a slot, completing on `bar`; the first one's page is known
-        const auto load = [&](int j, uint32_t dst, uint32_t bar, int page, int row, auto pair) {
-          constexpr bool P = decltype(pair)::value;
-          tma_load_5d<P>(dst, map, bar, 0, row, half, w.h, page);
-          if (split) tma_load_5d<P>(dst + C::kKHalf, map, bar, 0, row, 1, w.h, page);
-          for (int r = rows; r < part; r += rows) {
-            look_up(key_tile(w, j) * kKeys + first + r, page, row);
-            tma_load_5d<P>(dst + r * 128, map, bar, 0, row, half, w.h, page);
-            if (split) tma_load_5d<P>(dst + C::kKHalf + r * 128, map, bar, 0, row, 1, w.h, page);
-          }
-        };
-        int page, row;  // of the next tile's first box: looked up a step before they are used
-        look_up(key_tile(w, 0) * kKeys + first, page, row);
-        // the last V tile is completed in shared memory if it ends past kv_len
-        const int n = w.n - (kv == 1 && tail ? 1 : 0);
-        bool ok = true;
-        int slot = 0, issued = 0;
-        uint32_t phase = 0;
-        for (; issued < n; ++issued) {
-          ok = wait_bar(&empty[kv][slot], phase ^ 1u, abort_flag, p.status);
-          if (!ok) break;
-          if (rank == 0) mbar_arrive_expect_tx(&full[kv][slot], C::kBlocks * C::kSlot);
-          const int pg = page, rw = row;
-          load(issued, ring_kv + slot * C::kSlot, full_bar + 8 * slot, pg, rw,
-               std::integral_constant<bool, PAIR>());
-          if (issued + 1 < w.n) look_up(key_tile(w, issued + 1) * kKeys + first, page, row);
-          if (++slot == C::kSlots) { slot = 0; phase ^= 1u; }
+          const int end = min(w.len, w.pos0 + w.ntok);          // places any row sees
+          const int lo = p.window ? max(0, w.pos0 - p.window + 1) : 0;
+          const int32_t* table = p.block_table + (int64_t)x.t.b * p.max_pages;
+          // the last V tile is completed in shared memory if it ends past kv_len
+          const int n = x.s1 - (kv == 1 && x.tail ? 1 : 0);
+          const auto tiles = [&](auto row_boxes) {
+            constexpr int NR = decltype(row_boxes)::value;
+            // pages of a tile's boxes and their rows there (-1: no row of the unit sees the box),
+            // looked up a step before they are used
+            int page[NR], row[NR];
+            const auto look_up = [&](int j) {
+              const int key0 = key_tile(w, j) * kKeys + first;
+#pragma unroll
+              for (int b = 0; b < NR; ++b) {
+                const int key = key0 + b * rows;
+                page[b] = x.t.b;
+                row[b] = key;
+                if (key >= end || (key + rows <= lo && key >= p.n_sink)) {
+                  row[b] = -1;
+                } else if (p.block_table) {
+                  const int pg = (int)div_fast((uint32_t)key, p.page_div);
+                  page[b] = __ldg(table + pg);
+                  row[b] = key - pg * p.page_size;
+                }
+              }
+            };
+            const auto load = [&](uint32_t dst, uint32_t bar, auto pair) {
+              constexpr bool P = decltype(pair)::value;
+#pragma unroll
+              for (int b = 0; b < NR; ++b) {
+                int pg = page[b], rw = row[b];
+                if (rw < 0 || (uint32_t)pg >= (uint32_t)p.num_pages) {
+                  if (rw >= 0) record_error(p.status, MOE_ERR_DEVICE_BOUNDS);
+                  pg = p.num_pages;  // beyond the map: zeros
+                  rw = 0;
+                }
+                const uint32_t at = dst + b * rows * 128;
+                tma_load_5d<P>(at, map, bar, 0, rw, half, w.h, pg);
+                if (split) tma_load_5d<P>(at + C::kKHalf, map, bar, 0, rw, 1, w.h, pg);
+              }
+            };
+            if (x.s0 < x.s1) look_up(x.s0);
+            for (int j = x.s0; ok && j < x.s1; ++j) {
+              ok = wait_bar(&empty[kv][slot], phase ^ 1u, abort_flag, p.status);
+              if (!ok) break;
+              const uint32_t dst = ring_kv + slot * C::kSlot;
+              if (j < n) {
+                if (rank == 0)
+                  mbar_arrive_expect_tx(&full[kv][slot], C::kBlocks * C::kSlot);
+                else if (kv == 1)
+                  mbar_arrive_cluster(full_bar + 8 * slot);
+                load(dst, full_bar + 8 * slot, std::integral_constant<bool, PAIR>());
+              } else {
+                mbar_arrive_expect_tx(&tail_full, C::kSlot);
+                load(dst, smem_u32(&tail_full), std::integral_constant<bool, false>());
+              }
+              if (j + 1 < x.s1) look_up(j + 1);
+              ++issued;
+              if (++slot == C::kSlots) { slot = 0; phase ^= 1u; }
+            }
+          };
+          if (part == rows)
+            tiles(std::integral_constant<int, 1>());
+          else if (part == 2 * rows)
+            tiles(std::integral_constant<int, 2>());
+          else if (part == 4 * rows)
+            tiles(std::integral_constant<int, 4>());
+          else
+            tiles(std::integral_constant<int, 8>());
         }
-        if (ok && n < w.n) {
-          ok = wait_bar(&empty[kv][slot], phase ^ 1u, abort_flag, p.status);
-          if (ok) {
-            mbar_arrive_expect_tx(&tail_full, C::kSlot);
-            if (rank == 0) mbar_arrive(&full[kv][slot]);
-            load(n, ring_kv + slot * C::kSlot, smem_u32(&tail_full), page, row,
-                 std::integral_constant<bool, false>());
-            ++issued;
-            if (++slot == C::kSlots) { slot = 0; phase ^= 1u; }
-          }
-        }
-        // every load issued has landed before the block may exit (in pairs the even block's
-        // barriers count both blocks' bytes)
-        if (rank == 0) {
-          for (int s = 0; s < C::kSlots; ++s)
-            if (s < issued) drain_bar(&full[kv][s], s < slot ? phase : phase ^ 1u, p.status);
-          if (kv == 0)
-            for (int i = 0; i < 2; ++i)
-              if (i * span < w.ntok) drain_bar(&q_full[i], 0, p.status);
-        }
-        if (kv == 1 && tail && issued == w.n) drain_bar(&tail_full, 0, p.status);
-      }
-      __syncwarp();
-      if (kv == 0 && tail) {
-        // the places of the last V tile past kv_len: zeros
-        bool ok = wait_bar(&tail_full, 0, abort_flag, p.status);
         ok = __all_sync(0xffffffffu, ok);
-        if (ok) {
+        if (!ok) break;
+        ++units;
+        if (kv == 1 && x.tail) {
+          // the places of the last V tile past kv_len: zeros; only then has the tile arrived
+          ok = wait_bar(&tail_full, tails & 1, abort_flag, p.status);
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
+          ++tails;
+          const int lead = __ffs(__ballot_sync(0xffffffffu, issued > 0)) - 1;
+          const int at = (__shfl_sync(0xffffffffu, slot, lead) + C::kSlots - 1) % C::kSlots;
           const int r0 = w.len - key_tile(w, w.n - 1) * kKeys;
-          uint8_t* vt = ring + (C::kSlots + (w.n - 1) % C::kSlots) * C::kSlot;
-          for (int x = lane; x < (kKeys - r0) * 8; x += 32)
-            *reinterpret_cast<uint4*>(vt + (r0 + x / 8) * 128 + (x & 7) * 16) =
+          uint8_t* vt = ring + (C::kSlots + at) * C::kSlot;
+          for (int e = lane; e < (kKeys - r0) * 8; e += 32)
+            *reinterpret_cast<uint4*>(vt + (r0 + e / 8) * 128 + (e & 7) * 16) =
                 make_uint4(0, 0, 0, 0);
           fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0) {
             if (PAIR)
-              mbar_arrive_release_cluster(mapa_shared(smem_u32(&tail_ready), 0));
+              mbar_arrive_release_cluster(full_bar + 8 * at);
             else
-              mbar_arrive(&tail_ready);
+              mbar_arrive(&full[1][at]);
           }
         }
       }
-    } else if (w.n > 0 && (warp == 9 || warp == 11) && rank == 0) {
-      // ---------------- MMA: warp 9 row tile 0, warp 11 row tile 1 (one thread each) ----------------
+      // every load issued has landed before the block may exit (in pairs the even block's barriers
+      // count both blocks' bytes)
+      if (rank == 0) {
+        for (int s = 0; s < C::kSlots; ++s)
+          if (s < issued) drain_bar(&full[kv][s], s < slot ? phase : phase ^ 1u, p.status);
+        if (kv == 0 && units) drain_bar(&q_full, (units - 1) & 1, p.status);
+      }
+    } else if ((warp == 9 || warp == 11) && rank == 0) {
+      // ------------ MMA: warp 9 row tile 0, warp 11 row tile 1 (one thread each) ------------
       const int i = warp == 9 ? 0 : 1;
-      const RowTile rt = row_tile(p, w, i * span, span);
       const uint32_t idesc_s = idesc_bf16(kRows * C::kBlocks, kKeys);
       const uint32_t idesc_o = idesc_bf16_b_mn(kRows * C::kBlocks, D);
       const uint32_t s_t = tmem + i * 2 * kKeys, o_t = tmem + C::kTmemO + i * D;
@@ -436,9 +635,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           mma_commit(bar);
       };
       if (elect_one()) {
-        int n_qk = 0, n_pv = 0;  // products issued: the buffer and phase of the next
-        int ks = 0, vs = 0;      // slots of the next K and V tile
+        uint32_t n_qk = 0, n_pv = 0;  // products issued: the buffer and phase of the next
+        int ks = 0, vs = 0;           // slots of the next K and V tile
         uint32_t kp = 0, vp = 0;
+        uint32_t units = 0, seen = 0;
+        bool ok = true;
+        RowTile rt;
         // S = Q K(j); the K tile has arrived
         const auto qk = [&](int j) {
           if (!sees(rt, j)) return;
@@ -461,72 +663,93 @@ __global__ void __launch_bounds__(kThreads, 1)
           commit(&empty[0][ks]);
           if (++ks == C::kSlots) { ks = 0; kp ^= 1u; }
         };
-        bool ok = rt.ntok <= 0 || wait_bar(&q_full[i], 0, abort_flag, p.status);
-        for (int j = 0; ok && j < min(2, w.n); ++j) {
-          ok = wait_bar(&full[0][ks], kp, abort_flag, p.status);
+        Part x;
+        for (bool more = first_part(x); ok && more; more = next_part(x)) {
+          rt = row_tile(p, x.w, i * span, span, x.s0, x.s1);
+          ok = wait_bar(&q_full, units & 1, abort_flag, p.status);
           if (!ok) break;
-          tc_fence_after();
-          qk(j);
-          free_k();
-        }
-        for (int j = 0; ok && j < w.n; ++j) {
-          const bool more = j + 2 < w.n, pv = sees(rt, j);
-          // the operands first: once P is there, nothing else holds up the products
-          ok = wait_bar(&full[1][vs], vp, abort_flag, p.status);
-          if (ok && tail && j + 1 == w.n) ok = wait_bar_pair(&tail_ready, 0, abort_flag, p.status);
-          if (ok && more) ok = wait_bar(&full[0][ks], kp, abort_flag, p.status);
-          if (ok && pv) ok = wait_bar(&p_full[i][n_pv & 1], (n_pv >> 1) & 1, abort_flag, p.status);
-          if (!ok) break;
-          tc_fence_after();
-          if (pv) {  // O += P V(j)
-            const uint64_t dv = dv0 + (uint64_t)(vs * (int)(C::kSlot >> 4));
-            const uint32_t pa = s_t + (n_pv & 1) * kKeys;
-#pragma unroll
-            for (int kk = 0; kk < kKeys / 16; ++kk) {
-              const uint64_t at = dv + (uint64_t)(kk * (2048 >> 4));
-              const uint32_t acc = (n_pv || kk) ? 1u : 0u;
-              if (PAIR)
-                mma_ts_pair(o_t, pa + 8 * kk, at, idesc_o, acc);
-              else
-                mma_ts(o_t, pa + 8 * kk, at, idesc_o, acc);
-            }
-            ++n_pv;
+          for (int j = x.s0; ok && j < min(x.s0 + 2, x.s1); ++j) {
+            ok = wait_bar(&full[0][ks], kp, abort_flag, p.status);
+            if (!ok) break;
+            tc_fence_after();
+            qk(j);
+            free_k();
           }
-          if (more) qk(j + 2);
-          if (pv) commit(&o_full[i]);
-          if (j + 1 == rt.to) commit(&o_done[i]);
-          commit(&empty[1][vs]);
-          if (++vs == C::kSlots) { vs = 0; vp ^= 1u; }
-          if (more) free_k();
+          if (x.s1 - x.s0 <= 2) commit(&q_empty);
+          bool begun = false;
+          for (int j = x.s0; ok && j < x.s1; ++j) {
+            const bool ahead = j + 2 < x.s1, pv = sees(rt, j);
+            // the operands first: once P is there, nothing else holds up the products
+            ok = x.tail && j + 1 == x.s1 ? wait_bar_pair(&full[1][vs], vp, abort_flag, p.status)
+                                         : wait_bar(&full[1][vs], vp, abort_flag, p.status);
+            if (ok && ahead) ok = wait_bar(&full[0][ks], kp, abort_flag, p.status);
+            if (ok && pv && !begun) ok = wait_bar(&o_free[i], (seen & 1) ^ 1u, abort_flag, p.status);
+            if (ok && pv)
+              ok = wait_bar(&p_full[i][n_pv & 1], (n_pv >> 1) & 1, abort_flag, p.status);
+            if (!ok) break;
+            tc_fence_after();
+            if (pv) {  // O += P V(j)
+              const uint64_t dv = dv0 + (uint64_t)(vs * (int)(C::kSlot >> 4));
+              const uint32_t pa = s_t + (n_pv & 1) * kKeys;
+#pragma unroll
+              for (int kk = 0; kk < kKeys / 16; ++kk) {
+                const uint64_t at = dv + (uint64_t)(kk * (2048 >> 4));
+                const uint32_t acc = (begun || kk) ? 1u : 0u;
+                if (PAIR)
+                  mma_ts_pair(o_t, pa + 8 * kk, at, idesc_o, acc);
+                else
+                  mma_ts(o_t, pa + 8 * kk, at, idesc_o, acc);
+              }
+              ++n_pv;
+              begun = true;
+            }
+            if (ahead) qk(j + 2);
+            if (pv) commit(&o_full[i]);
+            if (j == rt.last) commit(&o_done[i]);
+            commit(&empty[1][vs]);
+            if (++vs == C::kSlots) { vs = 0; vp ^= 1u; }
+            if (ahead) {
+              free_k();
+              if (j + 3 == x.s1) commit(&q_empty);  // the unit's queries are read
+            }
+          }
+          ++units;
+          if (begun) ++seen;
         }
       }
       __syncwarp();
     }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
-    if (w.n >= 0) {
-      // ---------------- softmax and epilogue ----------------
-      const int i = warp >> 2;
-      const RowTile both = row_tile(p, w, i * span, span);  // the row tile over all blocks
-      const RowTile rt = row_tile(p, w, i * span + rank * p.TQ, p.TQ);
-      const int r = (warp & 3) * 32 + lane;                 // row of the tile
-      const int t = (int)div_fast((uint32_t)r, p.g_div);    // its token
-      const int pos = rt.p0 + t;
-      const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16);
-      const uint32_t o_t = lanes + C::kTmemO + i * D;
-      const uint32_t p_bar = PAIR ? mapa_shared(smem_u32(&p_full[i][0]), 0) : 0;
+    // ---------------- softmax and epilogue ----------------
+    const int i = warp >> 2;
+    const int r = (warp & 3) * 32 + lane;                 // row of the tile
+    const int t = (int)div_fast((uint32_t)r, p.g_div);    // its token
+    const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+    const uint32_t o_t = lanes + C::kTmemO + i * D;
+    const uint32_t p_bar = PAIR ? mapa_shared(smem_u32(&p_full[i][0]), 0) : 0;
+    const uint32_t o_bar = PAIR ? mapa_shared(smem_u32(&o_free[i]), 0) : 0;
+    uint32_t n = 0, seen = 0;  // tiles done; units seen anything of
+    bool ok = true;
+    Part x;
+    for (bool more = first_part(x); more; more = next_part(x)) {
+      const Work& w = x.w;
+      // the row tile over all blocks
+      const RowTile both = row_tile(p, w, i * span, span, x.s0, x.s1);
+      const int p0 = w.pos0 + i * span + rank * p.TQ;                 // of this block's rows
+      const int ntok = min(p.TQ, w.ntok - i * span - rank * p.TQ);
+      const int pos = p0 + t;
       const float sc2 = p.scale * kLog2e * (p.k_scale ? __ldg(p.k_scale + w.h) : 1.f);
-      // the running maximum and sum, the maximum as a base-2 exponent
-      float m = kNoMax, l = 0.f;
-      int n = 0;  // tiles done
-      bool ok = true;
       // key tiles whose every place every row sees: the first ones to, and of these those from (or
       // of sinks alone)
-      const int plain_to = (rt.p0 + 1) / kKeys;
-      const int plain_from = p.window ? max(0, rt.p1 - p.window + kKeys) / kKeys : 0;
+      const int plain_to = (p0 + 1) / kKeys;
+      const int plain_from = p.window ? max(0, p0 + ntok - 1 - p.window + kKeys) / kKeys : 0;
       const int plain_sink = p.n_sink / kKeys;
-      for (int j = both.sink ? 0 : both.from; ok && j < both.to;
-           j = j + 1 == both.sink ? both.from : j + 1) {
+      // the running maximum and sum, the maximum as a base-2 exponent
+      float m = kNoMax, l = 0.f;
+      bool begun = false;
+      for (int j = both.a1 > both.a0 ? both.a0 : both.b0; j < both.b1 || j < both.a1;
+           j = j + 1 == both.a1 ? both.b0 : j + 1) {
         const int kt = key_tile(w, j);
         const int k0 = kt * kKeys;
         const bool plain = kt < plain_to && (kt >= plain_from || kt < plain_sink);
@@ -543,15 +766,18 @@ __global__ void __launch_bounds__(kThreads, 1)
         tmem_ld_max_wait32(s + 32, mx2[1]);
         if (!plain) {
           asm volatile("" ::: "memory");  // a branch: predicated, the selects would cost every tile
-          const int hi = pos - k0;                                  // columns up to hi are seen
-          const int lo = p.window ? hi - p.window : -1;             // and after lo
-          const int sk = p.n_sink - k0;                             // or before sk
+          // columns up to `hi` are seen, but for those up to `lo` that are not before `sk`
+          const int hi = pos - k0, lo = p.window ? hi - p.window : -1, sk = p.n_sink - k0;
+          const uint64_t seen = below(hi + 1) & ~(below(lo + 1) & ~below(sk));
 #pragma unroll
           for (int c = 0; c < kKeys; ++c)
-            if (c > hi || (c <= lo && c >= sk)) s[c] = 0xFF800000u;
-          mx2[0] = mx2[1] = -INFINITY;
+            if (!(seen >> c & 1)) s[c] = 0xFF800000u;
+          // the load's maximum is that of every column: good enough unless it would raise m
+          if (__any_sync(0xffffffffu, fmaxf(mx2[0], mx2[1]) * sc2 > m + 8.f)) {
+            mx2[0] = mx2[1] = -INFINITY;
 #pragma unroll
-          for (int c = 0; c < kKeys; ++c) mx2[c & 1] = fmaxf(mx2[c & 1], __uint_as_float(s[c]));
+            for (int c = 0; c < kKeys; ++c) mx2[c & 1] = fmaxf(mx2[c & 1], __uint_as_float(s[c]));
+          }
         }
         const float mx = fmaxf(mx2[0], mx2[1]) * sc2;
         // raise the running maximum only where it is exceeded by 2^8 (or has no value yet)
@@ -560,7 +786,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const float f = raise ? ex2(m - mx) : 1.f;
           if (raise) m = mx;
           l *= f;
-          if (n) {
+          if (begun) {
             ok = wait_bar(&o_full[i], (n - 1) & 1, abort_flag, p.status);  // PV of the tile before
             // (S of this tile came after the PV before that one: the phase is unambiguous)
             ok = __all_sync(0xffffffffu, ok);
@@ -606,40 +832,103 @@ __global__ void __launch_bounds__(kThreads, 1)
           else
             mbar_arrive(&p_full[i][n & 1]);
         }
+        begun = true;
         ++n;
       }
-      if (n && ok)
-        ok = __all_sync(0xffffffffu, wait_bar(&o_done[i], 0, abort_flag, p.status));
-      if (ok) {
+      if (!ok) break;
+      if (begun) {
+        ok = wait_bar(&o_done[i], seen & 1, abort_flag, p.status);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        ++seen;
         tc_fence_after();
-        const bool mine = r < p.G * p.TQ && t < rt.ntok;
-        const int64_t tok = w.tok0 + i * span + rank * p.TQ + t;
-        const int head = w.h * p.G + (r - t * p.G);
-        const float vsc = p.v_scale ? __ldg(p.v_scale + w.h) : 1.f;
-        const float inv = l == 0.f ? 0.f : vsc / l;
+      }
+      // O through shared memory, 128 bytes of a row at a time, so that a store writes whole lines:
+      // of 32 rows a thread each, every store would touch 32.
+      const bool whole = x.s0 == 0 && x.s1 == w.n;
+      const int rows_in = min(p.G * p.TQ, p.G * ntok);    // rows of this block's row tile
+      const int64_t part0 = part_row<C>(run, x.s0 > 0 ? 0 : 1, i, rank);
+      const int64_t tok0 = w.tok0 + i * span + rank * p.TQ;
+      uint8_t* st = stage + warp * C::kStage;
+      const float vsc = p.v_scale ? __ldg(p.v_scale + w.h) : 1.f;
+      const float inv = l == 0.f ? 0.f : vsc / l;
+      const auto put = [&](int chunk, uint32_t z0, uint32_t z1, uint32_t z2, uint32_t z3) {
+        *reinterpret_cast<uint4*>(st + lane * 128 + ((chunk ^ lane) & 7) * 16) =
+            make_uint4(z0, z1, z2, z3);
+      };
+      // the lane's rows when the warp writes: 8 lanes to a row, rows 4e + lane / 8
+      const int row0 = (warp & 3) * 32 + (lane >> 3), chunk = lane & 7;
+      const auto take = [&](int e) {
+        return *reinterpret_cast<const uint4*>(st + (4 * e + (lane >> 3)) * 128 +
+                                               ((chunk ^ (4 * e + (lane >> 3))) & 7) * 16);
+      };
+      if (whole) {
+        uint16_t* to[8];
 #pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const int row = row0 + 4 * e, tk = (int)div_fast((uint32_t)row, p.g_div);
+          to[e] = p.o + (tok0 + tk) * p.o_stride + (w.h * p.G + row - tk * p.G) * D + chunk * 8;
+        }
+        const uint64_t inv2 = f32x2(inv, inv);
+#pragma unroll
+        for (int c = 0; c < D; c += 64) {
+          uint32_t y[64];
+          if (begun) {
+            tmem_ld32(o_t + c, y);
+            tmem_ld32(o_t + c + 32, y + 32);
+            tmem_ld_wait32(y);
+            tmem_ld_wait32(y + 32);
+          }
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            uint32_t z[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              float a, b;
+              f32x2_split(mul_f32x2(f32x2(__uint_as_float(y[8 * e + 2 * k]),
+                                          __uint_as_float(y[8 * e + 2 * k + 1])), inv2), a, b);
+              z[k] = inv == 0.f ? 0u : pack_bf16(a, b);
+            }
+            put(e, z[0], z[1], z[2], z[3]);
+          }
+          __syncwarp();
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            if (row0 + 4 * e < rows_in) *reinterpret_cast<uint4*>(to[e] + c) = take(e);
+          __syncwarp();
+        }
+      } else if (begun) {
+        float* to = p.parts + (part0 + row0) * D + chunk * 4;
+#pragma unroll 1
         for (int c = 0; c < D; c += 32) {
           uint32_t y[32];
-          if (n) {
-            tmem_ld32(o_t + c, y);
-            tmem_ld_wait32(y);
-          }
-          if (mine) {
-            uint4* dst = reinterpret_cast<uint4*>(p.o + tok * p.o_stride + (int64_t)head * D + c);
+          tmem_ld32(o_t + c, y);
+          tmem_ld_wait32(y);
 #pragma unroll
-            for (int e = 0; e < 32; e += 8) {
-              uint32_t z[4];
+          for (int e = 0; e < 8; ++e) put(e, y[4 * e], y[4 * e + 1], y[4 * e + 2], y[4 * e + 3]);
+          __syncwarp();
 #pragma unroll
-              for (int k = 0; k < 4; ++k)
-                z[k] = inv == 0.f ? 0u
-                                  : pack_bf16(__uint_as_float(y[e + 2 * k]) * inv,
-                                              __uint_as_float(y[e + 2 * k + 1]) * inv);
-              dst[e / 8] = make_uint4(z[0], z[1], z[2], z[3]);
-            }
-          }
+          for (int e = 0; e < 8; ++e)
+            if (row0 + 4 * e < rows_in) *reinterpret_cast<uint4*>(to + 4 * e * D + c) = take(e);
+          __syncwarp();
         }
-        if (mine && p.lse)
-          p.lse[tok * p.Hq + head] = l == 0.f ? -INFINITY : m * kLn2 + logf(l);
+      }
+      if (r < rows_in) {
+        if (!whole)  // the run's first part if the unit began before it, else its second
+          p.part_ml[part0 + r] = make_float2(m, l);
+        else if (p.lse)
+          p.lse[(tok0 + t) * p.Hq + w.h * p.G + (r - t * p.G)] =
+              l == 0.f ? -INFINITY : m * kLn2 + logf(l);
+      }
+      if (begun) {  // the next unit's products may overwrite O
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          if (PAIR)
+            mbar_arrive_cluster(o_bar);
+          else
+            mbar_arrive(&o_free[i]);
+        }
       }
     }
   }
@@ -653,6 +942,65 @@ __global__ void __launch_bounds__(kThreads, 1)
       tmem_dealloc_pair(tmem, 512);
     else
       tmem_dealloc(tmem, 512);
+  }
+}
+
+// Joins the parts of the units that runs cut: kJoin blocks look at the cut between two runs, and the
+// cuts of one unit share its (row, eight columns) tasks, in the parts' order.
+constexpr int kJoin = 16;
+
+template <int D>
+__global__ void __launch_bounds__(256) k_attn_prefill_join(const PrefillParams p) {
+  using C = Cfg<D>;
+  const int unit_tok = 2 * p.TQ * C::kBlocks;
+  const int c = (int)blockIdx.x / kJoin + 1, mine = (int)blockIdx.x % kJoin;
+  pdl_wait_then_release();
+  const Cut cut = p.cuts[c];
+  if (cut.step == 0) return;
+  // The cuts inside the unit are those whose step is kMinPart .. n - kMinPart: from y to z - 1 in
+  // the row. Run c0 begins the unit, run c1 ends it.
+  const auto run_of = [&](int64_t x) {  // the run that place x falls into
+    const int64_t longer = cut.more * (cut.each + 1);
+    return (int)(x < longer ? div_s(x, cut.each + 1) : cut.more + div_s(x - longer, cut.each));
+  };
+  const Work w = work_of(p, cut.at, unit_tok);
+  const int64_t y = cut.x0 + kUnitCost + kMinPart * kKeys;
+  const int64_t z = cut.x0 + kUnitCost + (int64_t)(w.n - kMinPart + 1) * kKeys;
+  const int c0 = run_of(y - 1), c1 = run_of(z - 1);
+  const int tasks = w.ntok * p.G * (D / 8);
+  const int shares = (c1 - c0) * kJoin, share = (c - c0 - 1) * kJoin + mine;
+  const int t0 = (int)((int64_t)tasks * share / shares);
+  const int t1 = (int)((int64_t)tasks * (share + 1) / shares);
+  const float vsc = p.v_scale ? __ldg(p.v_scale + w.h) : 1.f;
+  for (int task = t0 + (int)threadIdx.x; task < t1; task += 256) {
+    const int row = task / (D / 8), col = task % (D / 8) * 8;
+    const int tk = (int)div_fast((uint32_t)row, p.g_div), g = row - tk * p.G;
+    // token tk lies in row tile tk / span, block (tk % span) / TQ of the pair
+    const int span = p.TQ * C::kBlocks, i = tk / span, rank = tk % span / p.TQ;
+    const int r = (tk - i * span - rank * p.TQ) * p.G + g;
+    float m = kNoMax, l = 0.f, sum[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+    for (int x = c0; x <= c1; ++x) {
+      const int64_t at = part_row<C>(x, x == c0 ? 1 : 0, i, rank) + r;
+      const float2 ml = __ldcg(p.part_ml + at);
+      if (ml.y == 0.f) continue;  // the row saw nothing of the part
+      const float4* src = reinterpret_cast<const float4*>(p.parts + at * D + col);
+      const float4 lo = __ldcg(src), hi = __ldcg(src + 1);
+      const float to = fmaxf(m, ml.x), f = ex2(m - to), e = ex2(ml.x - to);
+      const float v[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+      l = l * f + ml.y * e;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) sum[k] = fmaf(v[k], e, sum[k] * f);
+      m = to;
+    }
+    const float inv = l == 0.f ? 0.f : vsc / l;
+    const int64_t tok = w.tok0 + tk;
+    const int head = w.h * p.G + g;
+    uint32_t out[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) out[k] = pack_bf16(sum[2 * k] * inv, sum[2 * k + 1] * inv);
+    *reinterpret_cast<uint4*>(p.o + tok * p.o_stride + (int64_t)head * D + col) =
+        make_uint4(out[0], out[1], out[2], out[3]);
+    if (p.lse && col == 0) p.lse[tok * p.Hq + head] = l == 0.f ? -INFINITY : m * kLn2 + logf(l);
   }
 }
 
@@ -731,6 +1079,13 @@ cudaError_t encode_bf16(CUtensorMap* m, const void* base, int rank, const cuuint
   return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
+// key tiles of the longest unit that the shape allows
+int64_t prefill_tiles_most(const AttnDims& a) {
+  const int64_t places = (int64_t)a.max_pages * a.page_size;
+  const int64_t seen = a.window ? (int64_t)a.window + a.n_sink + 2 * kRows * 2 : places;
+  return (seen < places ? seen : places) / kKeys + 3;
+}
+
 template <int D>
 cudaError_t launch(const AttnDims& a, const void* q, const void* k, const void* v,
                    PrefillParams& p, int64_t page_stride, int64_t head_stride,
@@ -767,14 +1122,24 @@ cudaError_t launch(const AttnDims& a, const void* q, const void* k, const void* 
   auto kern = k_attn_prefill<D>;
   e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::kSmem);
   if (e != cudaSuccess) return e;
-  // units of two row tiles: the sum over sequences of ceil(n / unit) <= T / unit + B, and <= T
-  const int64_t most = (int64_t)a.T / (2 * C::kBlocks * p.TQ) + a.B;
-  const unsigned blocks =  // under 2^31 (host check)
-      (unsigned)(most < a.T ? most : a.T) * (unsigned)a.Hkv * C::kBlocks;
-  count_launches(1);
-  if (C::kPair)
-    return launch_pdl_cluster(kern, dim3(blocks), dim3(kThreads), C::kSmem, st, 2u, mq, mk, mv, p);
-  return launch_pdl(kern, dim3(blocks), dim3(kThreads), C::kSmem, st, mq, mk, mv, p);
+  // Units: the sum over sequences of ceil(n / unit) <= T / unit + B, and <= T, for each key head. Where
+  // no unit can be long enough to be cut, no more runs than units.
+  const int64_t of_head = (int64_t)a.T / (2 * C::kBlocks * p.TQ) + a.B;
+  const int64_t most = (of_head < a.T ? of_head : a.T) * a.Hkv;
+  const int64_t full_units = (int64_t)(a.T / (2 * C::kBlocks * p.TQ)) * a.Hkv;  // about as many
+  int runs = num_sms() / C::kBlocks;
+  if (runs > kPrefillMaxCtas / C::kBlocks) runs = kPrefillMaxCtas / C::kBlocks;
+  p.min_split = full_units >= runs ? kSplitMany : kSplitFew;
+  const bool cuts = prefill_tiles_most(a) >= p.min_split;
+  if (!cuts) p.cuts = nullptr;
+  if (!cuts && runs > most) runs = (int)most;
+  count_launches(cuts && runs > 1 ? 2 : 1);
+  const dim3 grid((unsigned)(runs * C::kBlocks));
+  e = C::kPair ? launch_pdl_cluster(kern, grid, dim3(kThreads), C::kSmem, st, 2u, mq, mk, mv, p)
+               : launch_pdl(kern, grid, dim3(kThreads), C::kSmem, st, mq, mk, mv, p);
+  if (e != cudaSuccess || !cuts || runs == 1) return e;
+  return launch_pdl(k_attn_prefill_join<D>, dim3((unsigned)(runs - 1) * kJoin), dim3(256), 0, st,
+                    p);
 }
 
 template <int D>
@@ -815,6 +1180,10 @@ cudaError_t launch_attn_prefill(const AttnDims& a, const void* q, const void* k_
   p.o = static_cast<uint16_t*>(o);
   p.lse = lse;
   p.status = reinterpret_cast<int*>(ws + L.status);
+  p.parts = reinterpret_cast<float*>(ws + L.prefill_parts);
+  p.part_ml = reinterpret_cast<float2*>(ws + L.prefill_ml);
+  static_assert(sizeof(Cut) <= kPrefillCutBytes, "workspace");
+  p.cuts = reinterpret_cast<Cut*>(ws + L.prefill_cuts);
   p.max_pages = a.max_pages;
   int64_t ps = a.page_stride, hs = a.head_stride, ts = a.token_stride;
   if (prefill_reads_pages(a)) {

@@ -63,6 +63,17 @@ CASES = [
     dict(lens=[5] * 90 + [400], new=[5] * 90 + [333], Hq=4, Hkv=2),
     dict(lens=[3000], new=[1200], Hq=16, Hkv=2),            # the ring of tiles goes round
     dict(lens=[3000], new=[1200], Hq=16, Hkv=2, D=64, kv="fp8", page=64),
+    # units that are cut along the keys: few rows over much, and more units than blocks
+    dict(lens=[9000], new=[1], Hq=8, Hkv=1),
+    dict(lens=[20011], new=[70], Hq=4, Hkv=1, page=64),
+    dict(lens=[7000, 3, 5001, 0, 2500], new=[33, 3, 1, 0, 2500], Hq=14, Hkv=2),
+    dict(lens=[9000, 8000], new=[5, 500], Hq=8, Hkv=2, D=64, page=32),
+    dict(lens=[9000, 100], new=[400, 100], Hq=8, Hkv=2, window=3000, sink=200),
+    dict(lens=[9000, 100], new=[400, 100], Hq=8, Hkv=2, D=64, window=1100, kv="fp8"),
+    dict(lens=[6000], new=[2], Hq=2, Hkv=2, page=7),
+    dict(lens=[1500] * 3, new=[1500] * 3, Hq=16, Hkv=2),
+    dict(lens=[40] * 700, new=[1] * 700, Hq=2, Hkv=1),
+    dict(lens=[70] * 300, new=[40] * 300, Hq=4, Hkv=2, D=64),
 ]
 
 
@@ -86,6 +97,14 @@ def test_prefill(kw):
     again = run(step)
     assert torch.equal(o.view(torch.int16), again[0].view(torch.int16))
     assert torch.equal(lse, again[1])
+
+
+def test_split_rows_that_see_nothing_of_a_part():
+    # a window that ends inside a part: some rows see nothing of the keys that a block walks, and
+    # padding rows see nothing at all
+    step = Step(lens=[6000, 30], new=[300, 40], Hq=2, Hkv=1, window=2000, sink=1500)
+    o, lse = run(step)
+    check_attention(step, o, lse, "parts", P_ROUND)
 
 
 def test_rising_scores_raise_the_running_maximum():
