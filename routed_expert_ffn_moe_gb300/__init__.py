@@ -19,7 +19,7 @@ __all__ = ["MoeError", "MoeShape", "MOE_W_BF16", "MOE_W_FP8_E4M3_B128", "MOE_W_M
            "moe_last_error_string", "shape_of", "MoeLayer", "EXPORTED",
            "MoeAttnShape", "MOE_KV_BF16", "MOE_KV_FP8_E4M3", "attn_shape",
            "moe_attn_workspace_size", "moe_attn_workspace_zero_bytes", "moe_attn_append",
-           "moe_attn_decode", "moe_attn_prefill"]
+           "moe_attn_decode", "moe_attn_prefill", "AttnLayer"]
 
 MOE_W_BF16, MOE_W_FP8_E4M3_B128, MOE_W_MXFP4_E8M0_B32 = 0, 1, 2
 WDTYPES = {"bf16": MOE_W_BF16, "fp8": MOE_W_FP8_E4M3_B128, "mxfp4": MOE_W_MXFP4_E8M0_B32}
@@ -368,3 +368,81 @@ class MoeLayer:
                        w["w2"], w.get("s2"), self.y_perm, self.ws, stream)
         moe_combine(s, self.y_perm, self.inv_slot, self.topk_w, self.y, self.ws, stream)
         return self.y
+
+
+class AttnLayer:
+    """The attention of one decoder layer between its qkv and its output projection, with the cache,
+    the rotation table and the workspace allocated once (torch, on `device`).
+
+    `forward(qkv, block_table, kv_len, q_start)` takes a step's projections, one row
+    [(Hq + 2 Hkv) * D] bf16 a token (query heads, key heads, value heads), appends keys and values
+    to the cache and returns o [T, Hq * D] bf16: attention of one token a sequence where q_start is
+    None, else of the ragged step that q_start [B + 1] describes. kv_len [B] counts the step's
+    tokens; block_table [B, max_pages] names each sequence's pages. All three are int32 CUDA
+    tensors. Out-of-range pages, lengths and positions are reported by `check()`.
+
+    max_batch and max_tokens bound the sequences and tokens of a step. norms: (q_norm, k_norm), [D]
+    bf16 each, or None; scales: (k_scale, v_scale), [Hkv] fp32 each, for an "fp8" cache.
+    """
+
+    def __init__(self, Hq, Hkv, D, num_pages, page_size=16, max_pages=256, max_batch=64,
+                 max_tokens=4096, kv_dtype="bf16", window=0, n_sink=0, rot_dim=None,
+                 rot_pairs=False, rope_base=10000.0, norms=None, scales=None, scale=0.0, eps=1e-6,
+                 device="cuda"):
+        import torch
+        self.Hq, self.Hkv, self.D = Hq, Hkv, D
+        row = (Hq + 2 * Hkv) * D
+        self.max_batch, self.max_tokens, self.max_pages = max_batch, max_tokens, max_pages
+        self.q_norm, self.k_norm = norms or (None, None)
+        self.k_scale, self.v_scale = scales or (None, None)
+        rot_dim = D if rot_dim is None else rot_dim
+        max_pos = page_size * max_pages
+        self._kw = dict(Hq=Hq, Hkv=Hkv, D=D, kv_dtype=kv_dtype, page_size=page_size,
+                        max_pages=max_pages, num_pages=num_pages, window=window, n_sink=n_sink,
+                        rot_dim=rot_dim, rot_pairs=rot_pairs, max_pos=max_pos, scale=scale,
+                        eps=eps, q_stride=row, k_stride=row, v_stride=row)
+        dev = torch.device(device)
+        dt = torch.bfloat16 if kv_dtype == "bf16" else torch.uint8
+        self.k_cache = torch.zeros(num_pages, Hkv, page_size, D, dtype=dt, device=dev)
+        self.v_cache = torch.zeros_like(self.k_cache)
+        freq = rope_base ** (-torch.arange(rot_dim // 2, dtype=torch.float64) / max(rot_dim // 2, 1))
+        ang = torch.arange(max_pos, dtype=torch.float64)[:, None] * freq
+        self.cos_sin = torch.cat([ang.cos(), ang.sin()], 1).float().contiguous().to(dev)
+        n = moe_attn_workspace_size(attn_shape(T=max_tokens, B=max_batch, **self._kw), True)
+        if n == 0:
+            raise MoeError(-1, "AttnLayer", moe_last_error_string())
+        self.ws = torch.empty(n, dtype=torch.uint8, device=dev)
+        self.ws[:moe_attn_workspace_zero_bytes()].zero_()
+        self.q_rot = torch.empty(max_tokens, Hq * D, dtype=torch.bfloat16, device=dev)
+        self.o = torch.empty(max_tokens, Hq * D, dtype=torch.bfloat16, device=dev)
+        self._shapes = {}
+
+    def forward(self, qkv, block_table, kv_len, q_start=None, positions=None, lse=None, stream=None):
+        T, B = qkv.shape[0], kv_len.shape[0]
+        if T > self.max_tokens or B > self.max_batch or block_table.shape[1] != self.max_pages:
+            raise ValueError(f"a step of {T} tokens, {B} sequences and tables of "
+                             f"{block_table.shape[1]} pages: the layer was made for "
+                             f"{self.max_tokens}, {self.max_batch} and {self.max_pages}")
+        s = self._shapes.get((T, B))
+        if s is None:
+            if len(self._shapes) >= 1024:
+                self._shapes.clear()
+            s = self._shapes[(T, B)] = attn_shape(T=T, B=B, **self._kw)
+        nq, nk = self.Hq * self.D, self.Hkv * self.D
+        at = qkv.data_ptr()
+        q, k, v = (at, at + 2 * nq, at + 2 * (nq + nk)) if T else (None, None, None)
+        o = self.o[:T]
+        moe_attn_append(s, q, k, v, self.q_norm, self.k_norm, self.cos_sin, positions, block_table,
+                        kv_len, q_start, self.k_scale, self.v_scale, self.q_rot, self.k_cache,
+                        self.v_cache, self.ws, stream)
+        if q_start is None:
+            moe_attn_decode(s, self.q_rot, self.k_cache, self.v_cache, self.k_scale, self.v_scale,
+                            block_table, kv_len, o, lse, self.ws, stream)
+        else:
+            moe_attn_prefill(s, self.q_rot, self.k_cache, self.v_cache, self.k_scale, self.v_scale,
+                             block_table, kv_len, q_start, o, lse, self.ws, stream)
+        return o
+
+    def check(self, stream=None):
+        """Raises MoeError if a step since the last check met something out of range."""
+        moe_check_device_status(self.ws, stream)
