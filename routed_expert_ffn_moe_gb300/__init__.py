@@ -126,9 +126,10 @@ def _ptr(t):
     """Device pointer of a torch tensor (or an int address, or None)."""
     if t is None:
         return None
-    if isinstance(t, int):
+    try:
+        return t.data_ptr()
+    except AttributeError:
         return t
-    return t.data_ptr()
 
 
 def _current_stream():
@@ -172,7 +173,7 @@ def moe_workspace_size(shape: MoeShape) -> int:
 
 
 def _ws(ws):
-    return _ptr(ws), (ws.numel() * ws.element_size() if hasattr(ws, "numel") else 0)
+    return _ptr(ws), getattr(ws, "nbytes", 0)
 
 
 def moe_route(shape, x, wg, bias, topk_idx, topk_w, ws, stream=None, ws_bytes=None):

@@ -52,6 +52,7 @@ using tc::drain_bar;
 constexpr int kRows = 128;           // rows of a block's row tile
 constexpr int kKeys = 64;            // places of a key tile
 constexpr int kThreads = 384;
+constexpr int kRegs = 168;            // of a thread at launch: 384 * 168 = 128 * (200 + 200 + 104)
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr float kNoMax = -3e38f;     // the maximum of no scores: finite, so that -inf - it is -inf
 
@@ -476,7 +477,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     return true;
   };
 
-  // Registers: 384 threads of 168 at launch = 128 * (200 + 200 + 104).
   if (warp >= 8) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
     if (warp == 8 || warp == 10) {
@@ -1120,6 +1120,12 @@ cudaError_t launch(const AttnDims& a, const void* q, const void* k, const void* 
   if (e == cudaSuccess) e = encode_bf16(&mv, v, 5, dims, str, box_v);
   if (e != cudaSuccess) return e;
   auto kern = k_attn_prefill<D>;
+  // the warps exchange registers: what they take has to be there at launch
+  static const int regs = [&] {
+    cudaFuncAttributes at{};
+    return cudaFuncGetAttributes(&at, kern) == cudaSuccess ? at.numRegs : 0;
+  }();
+  if (regs != kRegs) return cudaErrorInvalidConfiguration;
   e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::kSmem);
   if (e != cudaSuccess) return e;
   // Units: the sum over sequences of ceil(n / unit) <= T / unit + B, and <= T, for each key head. Where
