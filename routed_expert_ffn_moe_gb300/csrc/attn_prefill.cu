@@ -619,6 +619,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (s < issued) drain_bar(&full[kv][s], s < slot ? phase : phase ^ 1u, p.status);
         if (kv == 0 && units) drain_bar(&q_full, (units - 1) & 1, p.status);
       }
+      // and so have the arrivals that hand slots and queries back
+      if (__all_sync(0xffffffffu, ok)) {
+        for (int s = 0; s < C::kSlots; ++s)
+          if (s < issued) drain_bar(&empty[kv][s], s < slot ? phase : phase ^ 1u, p.status);
+        if (kv == 0 && units) drain_bar(&q_empty, (units - 1) & 1, p.status);
+      }
     } else if ((warp == 9 || warp == 11) && rank == 0) {
       // ------------ MMA: warp 9 row tile 0, warp 11 row tile 1 (one thread each) ------------
       const int i = warp == 9 ? 0 : 1;
