@@ -316,7 +316,7 @@ MOE_API moe_status moe_attn_decode(const moe_attn_shape* shape, const void* q,
  * Scores, the softmax's maximum and sum and the output are held in fp32; the probabilities enter
  * the product with v as bf16. What the cache holds at the places of a sequence must be finite
  * (a NaN there spreads to earlier tokens of its tile; beyond kv_len and left of the window it does
- * not). E4M3 caches, and bf16 caches whose pages are not a multiple of 8 tokens, are
+ * not). E4M3 caches, and bf16 caches whose pages are not a multiple of 16 tokens, are
  * first unpacked into the workspace (4 B Hkv max_pages page_size D bytes). */
 MOE_API moe_status moe_attn_prefill(const moe_attn_shape* shape, const void* q,
                                     const void* k_cache, const void* v_cache,

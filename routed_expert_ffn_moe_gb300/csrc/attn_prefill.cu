@@ -489,7 +489,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       constexpr int kKRows = kKeys / C::kHalves;
       const int rows = kv ? p.v_rows : p.k_rows;
       const int part = kv ? kKeys : kKRows;                 // places of the block's part
-      const bool split = kv == 0 && PAIR && rows < kKRows;  // halves in boxes of their own
       const int first = kv ? 0 : rank * kKRows;             // its first place of a tile
       const int half = kv && PAIR ? rank : 0;
       const CUtensorMap* map = kv ? &tm_v : &tm_k;
@@ -521,41 +520,45 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int32_t* table = p.block_table + (int64_t)x.t.b * p.max_pages;
           // the last V tile is completed in shared memory if it ends past kv_len
           const int n = x.s1 - (kv == 1 && x.tail ? 1 : 0);
-          const auto tiles = [&](auto row_boxes) {
+          const auto tiles = [&](auto row_boxes, auto halves) {
             constexpr int NR = decltype(row_boxes)::value;
-            // pages of a tile's boxes and their rows there (-1: no row of the unit sees the box),
-            // looked up a step before they are used
+            constexpr bool split = decltype(halves)::value;  // halves of K in boxes of their own
+            // pages of a tile's boxes and their rows there, looked up a step before they are used;
+            // bit b of `in`: some row of the unit sees box b (others come from beyond the map: zeros)
             int page[NR], row[NR];
+            uint32_t in = 0;
             const auto look_up = [&](int j) {
               const int key0 = key_tile(w, j) * kKeys + first;
+              in = 0;
 #pragma unroll
               for (int b = 0; b < NR; ++b) {
                 const int key = key0 + b * rows;
-                page[b] = x.t.b;
-                row[b] = key;
-                if (key >= end || (key + rows <= lo && key >= p.n_sink)) {
-                  row[b] = -1;
-                } else if (p.block_table) {
-                  const int pg = (int)div_fast((uint32_t)key, p.page_div);
-                  page[b] = __ldg(table + pg);
-                  row[b] = key - pg * p.page_size;
+                page[b] = p.num_pages;
+                row[b] = 0;
+                if (key < end && (key + rows > lo || key < p.n_sink)) {
+                  in |= 1u << b;
+                  page[b] = x.t.b;
+                  row[b] = key;
+                  if (p.block_table) {
+                    const int pg = (int)div_fast((uint32_t)key, p.page_div);
+                    page[b] = __ldg(table + pg);
+                    row[b] = key - pg * p.page_size;
+                  }
                 }
               }
             };
             const auto load = [&](uint32_t dst, uint32_t bar, auto pair) {
               constexpr bool P = decltype(pair)::value;
+              uint32_t out = 0;
 #pragma unroll
               for (int b = 0; b < NR; ++b) {
-                int pg = page[b], rw = row[b];
-                if (rw < 0 || (uint32_t)pg >= (uint32_t)p.num_pages) {
-                  if (rw >= 0) record_error(p.status, MOE_ERR_DEVICE_BOUNDS);
-                  pg = p.num_pages;  // beyond the map: zeros
-                  rw = 0;
-                }
+                const uint32_t pg = min((uint32_t)page[b], (uint32_t)p.num_pages);
+                if (pg == (uint32_t)p.num_pages) out |= 1u << b;
                 const uint32_t at = dst + b * rows * 128;
-                tma_load_5d<P>(at, map, bar, 0, rw, half, w.h, pg);
-                if (split) tma_load_5d<P>(at + C::kKHalf, map, bar, 0, rw, 1, w.h, pg);
+                tma_load_5d<P>(at, map, bar, 0, row[b], half, w.h, pg);
+                if (split) tma_load_5d<P>(at + C::kKHalf, map, bar, 0, row[b], 1, w.h, pg);
               }
+              if (out & in) record_error(p.status, MOE_ERR_DEVICE_BOUNDS);
             };
             if (x.s0 < x.s1) look_up(x.s0);
             for (int j = x.s0; ok && j < x.s1; ++j) {
@@ -577,14 +580,15 @@ __global__ void __launch_bounds__(kThreads, 1)
               if (++slot == C::kSlots) { slot = 0; phase ^= 1u; }
             }
           };
+          using std::integral_constant;
           if (part == rows)
-            tiles(std::integral_constant<int, 1>());
+            tiles(integral_constant<int, 1>(), std::false_type());
+          else if (PAIR && kv == 0)
+            tiles(integral_constant<int, 2>(), std::true_type());
           else if (part == 2 * rows)
-            tiles(std::integral_constant<int, 2>());
-          else if (part == 4 * rows)
-            tiles(std::integral_constant<int, 4>());
+            tiles(integral_constant<int, 2>(), std::false_type());
           else
-            tiles(std::integral_constant<int, 8>());
+            tiles(integral_constant<int, 4>(), std::false_type());
         }
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
@@ -1113,7 +1117,7 @@ cudaError_t launch(const AttnDims& a, const void* q, const void* k, const void* 
                              (cuuint64_t)page_stride * 2};
   // boxes of whole pages, or of the places of a tile that lie in one page
   const auto rows = [&](int most) {
-    int r = 8;
+    int r = 16;
     while (r < most && p.page_size % (2 * r) == 0) r *= 2;
     return r;
   };
