@@ -22,13 +22,19 @@
 // item ends, when they merge through the stage that was just consumed.
 //
 // Probabilities of a bf16 cache enter the product with v as two bf16 terms (2^-16 relative): the
-// tensor cores have room, and one term alone would be the largest error of the result.
+// tensor cores have room, and one term alone would be the largest error of the result. Those of an
+// E4M3 cache are one f16 term (2^-12 relative): its codes carry 2^-4 themselves.
 //
 // E4M3 codes enter the MMAs as f16 (exactly). The queries become f16 too, each row times the
 // power of two that brings its largest element to [2^14, 2^15), taken back in the scores'
 // scale: elements above 2^-28 of the row's largest are exact. An 8-bit row is read in 16-bit
 // pairs, which permutes the contraction index of q.k (the queries are loaded in the same order)
 // and the columns of v (stored back in place).
+//
+// Measured, of a copy rate of 6772 GB/s, 8 key heads of 128, 64 query heads: 256 sequences of 2048
+// to 8192 places, bf16, 805 us, 0.99; one of 131071, 89 us, 0.89, of 524288, 320 us, 0.99; 64
+// sequences of 2048 places in E4M3, 64 us, 0.62, of 32768, 779 us, 0.81 (the conversions and the
+// 8 warps that the registers leave an SM); one of 1003 places, 7.3 us: the start of two kernels.
 #include "attn.h"
 #include "sm100_ptx.cuh"
 
@@ -127,9 +133,15 @@ struct Cfg {
   static constexpr int kHalfBytes = kKeys * kRowBytes; // a warp's keys (or values) of a stage
   static constexpr int kStageBytes = 2 * kHalfBytes;   // a warp's output rows fit for the merge
   static constexpr int kLook = kKeys > 32 ? kKeys / 32 : 1;  // keys that a lane looks up
-  static constexpr int kStages = 3;
+  // Resident blocks of an SM, which share its registers and shared memory: three of two stages
+  // where a warp's fragments fit in 168 registers and the conversions of E4M3 keep it busier than
+  // the loads, else two of three. 96 sequences of 2 key heads of 64, E4M3, three against two, us:
+  // 32768 places 158 against 175, 8192 51 against 53, 1024 14.3 against 13.9; bf16, 258 against
+  // 255, 73 against 73, 17.2 against 16.2. 64 sequences of 8 key heads of 128, E4M3: 715 against
+  // 779, 200 against 210, but 72 against 64 at 2048 (they spill, and items end more often).
+  static constexpr int kBlocks = FP8 && D == 64 ? 3 : 2;
+  static constexpr int kStages = kBlocks == 3 ? 2 : 3;
   static constexpr int kSmem = kWarps * kStages * kStageBytes;
-  static constexpr int kBlocks = 2;                    // resident blocks of an SM
   static_assert(kStageBytes >= kDecodeRows * D * 4, "merge area");
 };
 
@@ -646,7 +658,10 @@ __global__ void __launch_bounds__(kThreads, C::kBlocks) k_attn_decode(const Deco
 // Joins the parts of the items that span blocks. Block c - 1 looks at the boundary between blocks c - 1
 // and c of k_attn_decode: if it lies inside an item, the blocks of that item's boundaries share its
 // (row, eight columns) tasks; the lanes of a group take a task's parts in turn, each with a running
-// maximum, and meet in a butterfly.
+// maximum, and meet in a butterfly. Bound by latency: its blocks find their boundary while
+// k_attn_decode runs, and joining in k_attn_decode instead (the last block to arrive joins an item) took
+// 9.5 us against 7.5 for one sequence of 1003 places, and with one key head over 131072 places, whose
+// parts then all fall to one block, 211 against 27.
 template <class C>
 __global__ void __launch_bounds__(kThreads) k_attn_join(const DecodeParams p) {
   constexpr int D = C::D;
