@@ -1,5 +1,6 @@
 /*
- * moe.h -- C ABI of the GB300 (sm_103a) routed-expert MoE FFN layer, inference hot path.
+ * moe.h -- C ABI of the GB300 (sm_103a) routed-expert MoE FFN layer, inference hot path, and of the
+ * attention over a paged cache that stands before it in a decoder layer (moe_attn_*, at the end).
  *
  * The layer, as the pages state it:
  *   router     -- score every routed expert for each token, keep the top-k
@@ -230,7 +231,8 @@ MOE_API moe_status moe_forward(const moe_shape* shape, const void* x, const void
  * of n has place kv_len[b] - n + i (a negative place is padding: nothing is cached for it and
  * its output is zero). Place p sees place j if j <= p and (window = 0 or p - j < window or
  * j < n_sink). block_table entries of pages that hold no visible place are not read; what the
- * cache holds beyond kv_len or outside the window never reaches a result.
+ * cache holds beyond kv_len never reaches a result, nor what it holds outside the window but for
+ * moe_attn_prefill's tiles (see there).
  *
  * q_start, kv_len, block_table and positions are DEVICE int32 arrays and are checked there: a
  * page outside [0, num_pages), a length beyond the table or a rotary position outside
@@ -314,10 +316,12 @@ MOE_API moe_status moe_attn_decode(const moe_attn_shape* shape, const void* q,
  *   q [T, Hq, D] bf16, o [T, Hq, D] bf16 out, lse [T, Hq] fp32 out or NULL; rows of o and lse from
  *   q_start[B] on are not written. A token that sees no place gives o = 0 and lse = -inf.
  * Scores, the softmax's maximum and sum and the output are held in fp32; the probabilities enter
- * the product with v as bf16. What the cache holds at the places of a sequence must be finite
- * (a NaN there spreads to earlier tokens of its tile; beyond kv_len and left of the window it does
- * not). E4M3 caches, and bf16 caches whose pages are not a multiple of 16 tokens, are
- * first unpacked into the workspace (4 B Hkv max_pages page_size D bytes). */
+ * the product with v as bf16. What the cache holds at the places of a sequence must be finite:
+ * 0 times a NaN or an infinity of v is a NaN, so one spreads to the tokens of its tile (128 / G
+ * or more tokens, 64 places) that do not see it. Beyond kv_len, and in pages that no token of
+ * the step sees anything of, it does not. E4M3 caches, and bf16 caches whose pages are not a
+ * multiple of 16 tokens, are first unpacked into the workspace
+ * (4 B Hkv max_pages page_size D bytes, max_pages page_size rounded up to 128). */
 MOE_API moe_status moe_attn_prefill(const moe_attn_shape* shape, const void* q,
                                     const void* k_cache, const void* v_cache,
                                     const float* k_scale, const float* v_scale,
