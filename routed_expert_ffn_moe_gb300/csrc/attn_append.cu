@@ -24,9 +24,11 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kBatch = 4;  // heads of a batch
-// Head rows (tokens x heads) of a small step. Of 72 heads an E4M3 step takes, small kernel against large:
-// 64 tokens 3.0 against 4.8 us, 256 tokens 5.9 against 6.4, 1024 tokens 19.9 against 19.6.
-constexpr int64_t kSmallRows = 1 << 16;
+// Lanes (tokens x heads x D / 8) of a small step. Small kernel against large, us, bf16, query + key
+// heads: of 64, 4+1, 4096 tokens 5.2 against 18.3, 16384 13.8 against 19.9; 32+8, 1024 tokens 6.7
+// against 10.5, 4096 23.2 against 23.6; 64+8, 4096 38 against 29. Of 128, 4+1, 16384 tokens 24.1
+// against 24.2; 32+8, 256 tokens 4.7 against 5.3, 1024 11.6 against 11.8, 4096 47 against 32.
+constexpr int64_t kSmallLanes = 9 << 17;
 
 struct AppendParams {
   AttnDims a;
@@ -46,7 +48,8 @@ struct AppendParams {
   uint8_t* k_cache;
   uint8_t* v_cache;
   int* status;
-  int groups;  // lane groups of a token in a block (a power of two)
+  int groups;  // large: lane groups of a token in a block (a power of two)
+  FastDiv heads_div;  // small: by the heads of a token, of all kinds
 };
 
 __device__ __forceinline__ void unpack8(const uint4& u, float (&x)[8]) {
@@ -321,30 +324,31 @@ __global__ void __launch_bounds__(kThreads, 3) k_attn_append(const AppendParams 
   }
 }
 
-// Small steps: one head to a lane group. Short code, many blocks: such a step is the latency of
-// its chain of look-ups.
+// Small steps: one head to a lane group, tokens and heads in a row. Short code, many blocks: such a
+// step is the latency of its chain of look-ups. 1 token of 32 + 8 + 8 heads of 128: 2.3 us; 256 of 56 +
+// 8 + 8, E4M3: 5.9 us.
 template <int D, bool FP8>
 __global__ void __launch_bounds__(kThreads, 5) k_attn_append_small(const AppendParams p) {
   constexpr int LPH = D / 8, GROUPS = kThreads / LPH;
   const AttnDims& a = p.a;
   const int sub = (int)threadIdx.x % LPH, heads = a.Hq + 2 * a.Hkv;
-  const int h = (int)blockIdx.y * GROUPS + (int)threadIdx.x / LPH, t = (int)blockIdx.x;
+  const uint32_t row = blockIdx.x * GROUPS + threadIdx.x / LPH;
+  const int tok = (int)div_fast(row, p.heads_div), h = (int)row - tok * heads, t = min(tok, a.T - 1);
   const bool is_q = h < a.Hq, is_v = h >= a.Hq + a.Hkv;
   const int hk = is_q ? h : is_v ? h - a.Hq - a.Hkv : h - a.Hq;  // among its kind
-  const uint16_t* row = is_q   ? p.q + (int64_t)t * a.q_stride
+  const uint16_t* src = is_q   ? p.q + (int64_t)t * a.q_stride
                         : is_v ? p.v + (int64_t)t * a.v_stride
                                : p.k + (int64_t)t * a.k_stride;
   const uint16_t* w = is_v ? nullptr : is_q ? p.q_norm : p.k_norm;
   pdl_wait_then_release();
-  uint4 u = make_uint4(0, 0, 0, 0);
-  if (h < heads) u = *reinterpret_cast<const uint4*>(row + (int64_t)hk * D + sub * 8);
-  const Place at = find_place<LPH>(p, t);
+  const uint4 u = *reinterpret_cast<const uint4*>(src + (int64_t)hk * D + sub * 8);
+  const Place at = find_place<LPH>(p, tok);
   Turn k;
   coefficients<LPH>(p, at, w, k);
   float z[8];
   // a warp holds several heads, of any kinds: the lanes exchange for all of them
   turn_head<LPH>(a, k, p.q_norm != nullptr || p.k_norm != nullptr, w != nullptr, u, z);
-  if (h >= heads) return;
+  if (tok >= a.T) return;
   if (is_q) {
     *reinterpret_cast<uint4*>(p.q_out + (int64_t)t * a.qr_stride + (int64_t)h * D + sub * 8) =
         at.live ? pack8_bf16(z) : make_uint4(0, 0, 0, 0);
@@ -362,10 +366,11 @@ cudaError_t launch(AppendParams& p, cudaStream_t st) {
   const int heads = p.a.Hq + 2 * p.a.Hkv;
   const int64_t rows = (int64_t)p.a.T * heads;
   count_launches(1);
-  if (rows <= kSmallRows)
-    return launch_pdl(k_attn_append_small<D, FP8>,
-                      dim3((unsigned)p.a.T, (unsigned)((heads + GROUPS - 1) / GROUPS)),
+  if (rows * (D / 8) <= kSmallLanes) {
+    p.heads_div = fast_div((uint32_t)heads);
+    return launch_pdl(k_attn_append_small<D, FP8>, dim3((unsigned)((rows + GROUPS - 1) / GROUPS)),
                       dim3(kThreads), 0, st, p);
+  }
   // Fewer groups a token mean fewer look-ups and more heads a group, as long as the blocks fill the
   // SMs several times.
   p.groups = GROUPS;
