@@ -25,10 +25,10 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kBatch = 4;  // heads of a batch
 // Lanes (tokens x heads x D / 8) of a small step. Small kernel against large, us, bf16, query + key
-// heads: of 64, 4+1, 4096 tokens 5.2 against 18.3, 16384 13.8 against 19.9; 32+8, 1024 tokens 6.7
-// against 10.5, 4096 23.2 against 23.6; 64+8, 4096 38 against 29. Of 128, 4+1, 16384 tokens 24.1
-// against 24.2; 32+8, 256 tokens 4.7 against 5.3, 1024 11.6 against 11.8, 4096 47 against 32.
-constexpr int64_t kSmallLanes = 9 << 17;
+// heads: of 64, 4+1, 1024 tokens 2.8 against 4.3, 4096 5.3 against 4.7; 64+8, 256 tokens 3.6 against
+// 4.1, 1024 9.6 against 8.6. Of 128, 4+1, 1024 tokens 3.5 against 4.3, 2048 5.4 against 4.7; 64+8, 64
+// tokens 3.0 against 4.8, 256 5.8 against 6.1, 1024 18.7 against 12.4.
+constexpr int64_t kSmallLanes = 5 << 16;
 
 struct AppendParams {
   AttnDims a;
@@ -286,12 +286,17 @@ __global__ void __launch_bounds__(kThreads, 3) k_attn_append(const AppendParams 
   fetch(q_row, h0, a.Hq, u);
   const Place at = find_place<LPH>(p, tok);
 
-  const auto turned = [&](const uint16_t* row, int heads, const uint16_t* w, const auto& put) {
+  // the last batch of a kind asks for the first of the next kind
+  const auto turned = [&](const uint16_t* row, int heads, const uint16_t* w, const uint16_t* then,
+                          const auto& put) {
     Turn k;
     coefficients<LPH>(p, at, w, k);
     for (int base = 0; base < heads; base += kBatch * step) {  // the same rounds for everyone
       uint4 next[kBatch];
-      fetch(row, base + kBatch * step + h0, heads, next);
+      if (base + kBatch * step < heads)
+        fetch(row, base + kBatch * step + h0, heads, next);
+      else
+        fetch(then, h0, a.Hkv, next);
 #pragma unroll
       for (int i = 0; i < kBatch; ++i) {
         if (base + i * step >= heads) break;  // for the whole block
@@ -304,16 +309,15 @@ __global__ void __launch_bounds__(kThreads, 3) k_attn_append(const AppendParams 
       for (int i = 0; i < kBatch; ++i) u[i] = next[i];
     }
   };
-  turned(q_row, a.Hq, p.q_norm, [&](int h, const float (&z)[8]) {
+  turned(q_row, a.Hq, p.q_norm, k_row, [&](int h, const float (&z)[8]) {
     *reinterpret_cast<uint4*>(p.q_out + (int64_t)t * a.qr_stride + (int64_t)h * D + sub * 8) =
         at.live ? pack8_bf16(z) : make_uint4(0, 0, 0, 0);
   });
-  fetch(k_row, h0, a.Hkv, u);
-  turned(k_row, a.Hkv, p.k_norm, [&](int h, const float (&z)[8]) {
+  turned(k_row, a.Hkv, p.k_norm, v_row, [&](int h, const float (&z)[8]) {
     store_cache<FP8>(p, p.k_cache, p.k_scale, at.slot, h, sub * 8, z);
   });
   for (int h = h0; h < a.Hkv; h += kBatch * step) {
-    fetch(v_row, h, a.Hkv, u);
+    if (h != h0) fetch(v_row, h, a.Hkv, u);
 #pragma unroll
     for (int i = 0; i < kBatch; ++i) {
       if (h + i * step >= a.Hkv) break;
@@ -371,10 +375,15 @@ cudaError_t launch(AppendParams& p, cudaStream_t st) {
     return launch_pdl(k_attn_append_small<D, FP8>, dim3((unsigned)((rows + GROUPS - 1) / GROUPS)),
                       dim3(kThreads), 0, st, p);
   }
-  // Fewer groups a token mean fewer look-ups and more heads a group, as long as the blocks fill the
-  // SMs several times.
+  // Fewer groups a token mean fewer look-ups and more heads a group: no more groups than batches of
+  // query heads; 16 query heads a group as long as that fills the SMs' places (three blocks each);
+  // and more where the blocks would fill them eight times over. 64 + 8 heads of 128, 4096 tokens,
+  // 16, 8, 4 groups: 38.7, 36.8, 34.0 us; 16384 tokens, 4, 2, 1: 109.8, 107.7, 114.3. 14 + 2 heads of 64,
+  // 4096 tokens, 32, 2: 18.5, 7.7.
   p.groups = GROUPS;
-  while (p.groups > 1 && (int64_t)p.a.T * p.groups / GROUPS > 24 * (int64_t)num_sms())
+  const auto blocks = [&] { return (int64_t)p.a.T * p.groups / GROUPS; };
+  while (p.groups > 1 && (p.groups * kBatch > p.a.Hq || blocks() > 24 * num_sms() ||
+                          (p.groups * 8 >= p.a.Hq && blocks() >= 6 * num_sms())))
     p.groups >>= 1;
   const int per_block = GROUPS / p.groups;
   return launch_pdl(k_attn_append<D, FP8>, dim3((unsigned)((p.a.T + per_block - 1) / per_block)),
