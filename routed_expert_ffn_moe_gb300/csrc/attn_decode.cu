@@ -307,12 +307,13 @@ __global__ void __launch_bounds__(kThreads, C::kBlocks) k_attn_decode(const Deco
   uint8_t* ring = smem + warp * (C::kStages * C::kStageBytes);
   const uint32_t ring_u = smem_u32(ring);
 
-  // the pages of this lane's keys (lane, lane + 32) of unit `c` (-1: not visible), and their rows
+  // the pages of this lane's keys (lane, lane + 32) of unit `c`, and their rows (-1: not visible);
+  // nothing here waits for a page
   const auto look_up = [&](const Cursor& c, int64_t u, int (&page)[C::kLook], int (&row)[C::kLook]) {
 #pragma unroll
     for (int i = 0; i < C::kLook; ++i) {
-      page[i] = -1;
-      row[i] = 0;
+      page[i] = 0;
+      row[i] = -1;
       const int key = 32 * i + lane;
       if (u >= u1 || key >= C::kKeys) continue;
       const bool in_sink = c.tile < c.s.ts;
@@ -322,10 +323,6 @@ __global__ void __launch_bounds__(kThreads, C::kBlocks) k_attn_decode(const Deco
       const int pg = (int)div_fast((uint32_t)j, a.page_div);
       row[i] = j - pg * a.page_size;
       page[i] = __ldg(p.block_table + (int64_t)c.b * a.max_pages + pg);
-      if ((uint32_t)page[i] >= (uint32_t)a.num_pages) {
-        record_error(p.status, MOE_ERR_DEVICE_BOUNDS);
-        page[i] = -1;
-      }
     }
   };
   // copies this warp's keys and values of a unit into stage st
@@ -334,10 +331,14 @@ __global__ void __launch_bounds__(kThreads, C::kBlocks) k_attn_decode(const Deco
     constexpr int RP = 32 / CH;  // rows of a pass
     int64_t mine[C::kLook];
 #pragma unroll
-    for (int i = 0; i < C::kLook; ++i)
-      mine[i] = page[i] < 0 ? -1
-                            : (int64_t)page[i] * a.page_stride + (int64_t)row[i] * a.token_stride +
-                                  (int64_t)(c.hr / p.rt) * a.head_stride;
+    for (int i = 0; i < C::kLook; ++i) {
+      const bool there = (uint32_t)page[i] < (uint32_t)a.num_pages;
+      if (row[i] >= 0 && !there) record_error(p.status, MOE_ERR_DEVICE_BOUNDS);
+      mine[i] = row[i] < 0 || !there ? -1
+                                     : (int64_t)page[i] * a.page_stride +
+                                           (int64_t)row[i] * a.token_stride +
+                                           (int64_t)(c.hr / p.rt) * a.head_stride;
+    }
     const int chunk = lane % CH;
     const uint32_t dst = ring_u + st * C::kStageBytes;
 #pragma unroll
@@ -351,20 +352,6 @@ __global__ void __launch_bounds__(kThreads, C::kBlocks) k_attn_decode(const Deco
       cp_async16(to + C::kHalfBytes, p.v_cache + at, live);
     }
   };
-
-  // ---- fill the ring ----
-  int page[C::kLook], row[C::kLook];
-  int64_t lu = cu;  // unit of the load cursor
-  look_up(lc, lu, page, row);
-#pragma unroll
-  for (int st = 0; st < C::kStages; ++st) {
-    if (lu < u1) {
-      copy_in(lc, page, row, st);
-      lu += advance<TILE>(p, hr_n, lc);
-      look_up(lc, lu, page, row);
-    }
-    cp_async_commit();
-  }
 
   uint32_t qf[KS][4];
   float acc[NT][4];
@@ -387,6 +374,30 @@ __global__ void __launch_bounds__(kThreads, C::kBlocks) k_attn_decode(const Deco
   };
   bool fresh = true;
   if (cu < u1) load_q(cc);
+
+  // ---- fill the ring: all look-ups first, so that their latencies pass together ----
+  int page[C::kLook], row[C::kLook];
+  int64_t lu = cu;  // unit of the load cursor
+  {
+    Cursor at[C::kStages];
+    int pages[C::kStages][C::kLook], rows_of[C::kStages][C::kLook];
+    bool is[C::kStages];
+#pragma unroll
+    for (int st = 0; st < C::kStages; ++st) {
+      is[st] = lu < u1;
+      if (is[st]) {
+        at[st] = lc;
+        look_up(lc, lu, pages[st], rows_of[st]);
+        lu += advance<TILE>(p, hr_n, lc);
+      }
+    }
+    look_up(lc, lu, page, row);
+#pragma unroll
+    for (int st = 0; st < C::kStages; ++st) {
+      if (is[st]) copy_in(at[st], pages[st], rows_of[st], st);
+      cp_async_commit();
+    }
+  }
 
   int st = 0;
   while (cu < u1) {
