@@ -261,7 +261,7 @@ __device__ __forceinline__ void store_cache(const AppendParams& p, uint8_t* cach
 }
 
 // Large steps: a lane group takes the heads of its token in turn, `groups` of them to a token. 16245
-// tokens of 64 + 8 + 8 heads of 128: 106 us, 0.93 of the measured copy rate.
+// tokens of 64 + 8 + 8 heads of 128: 106 us, 0.93 of the measured copy rate; 4096, 34 us, 0.73.
 template <int D, bool FP8>
 __global__ void __launch_bounds__(kThreads, 3) k_attn_append(const AppendParams p) {
   constexpr int LPH = D / 8, GROUPS = kThreads / LPH;

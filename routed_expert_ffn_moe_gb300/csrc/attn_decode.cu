@@ -32,9 +32,9 @@
 // and the columns of v (stored back in place).
 //
 // Measured, of a copy rate of 6772 GB/s, 8 key heads of 128, 64 query heads: 256 sequences of 2048
-// to 8192 places, bf16, 805 us, 0.99; one of 131071, 89 us, 0.89, of 524288, 320 us, 0.99; 64
-// sequences of 2048 places in E4M3, 64 us, 0.62, of 32768, 779 us, 0.81 (the conversions and the
-// 8 warps that the registers leave an SM); one of 1003 places, 7.3 us: the start of two kernels.
+// to 8192 places, bf16, 798 us, 1.0; one of 131071, 88 us, 0.90, of 524288, 318 us, 1.0; 64 sequences
+// of 2048 places in E4M3 pages of 16, 64 us, 0.63, of 32768, 767 us, 0.83 (runs of 2 KB, the conversions,
+// and the 8 warps that the registers leave an SM); one of 1003 places, 7.2 us: the start of two kernels.
 #include "attn.h"
 #include "sm100_ptx.cuh"
 
