@@ -144,7 +144,8 @@ __device__ __forceinline__ uint64_t add_f32x2(uint64_t a, uint64_t b) {
 // tiles stay whole, else of less than 16. Cut against whole, us: 1024 units of 18 tiles 129 against
 // 122; 8 prompts of 1024 tokens (512 units of up to 17) 158 against 141; 256 units of up to 345, 828
 // against 948. With few units: 16 tokens over 8192 places 32 against 79, over 2048 23 against 26;
-// of up to 9 tiles, 512 tokens, 28 against 21.
+// of up to 9 tiles, 512 tokens, 28 against 21. A unit's start and end weighed as 4, 6, 8 tiles, us: 8
+// ragged prompts 320, 327, 343; one of 2048 tokens 66, 74, 72; one over 20011 places 806, 801, 820.
 constexpr int kUnitCost = 4 * kKeys, kMinPart = 4, kSplitFew = 16, kSplitMany = 48;
 
 // n / d of non-negative numbers: a 32-bit division where both fit
