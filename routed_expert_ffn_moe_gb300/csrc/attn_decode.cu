@@ -669,7 +669,8 @@ __global__ void __launch_bounds__(kThreads, C::kBlocks) k_attn_decode(const Deco
 // Joins the parts of the items that span blocks. Block c - 1 looks at the boundary between blocks c - 1
 // and c of k_attn_decode: if it lies inside an item, the blocks of that item's boundaries share its
 // (row, eight columns) tasks; the lanes of a group take a task's parts in turn, each with a running
-// maximum, and meet in a butterfly. Bound by latency: its blocks find their boundary while
+// maximum, and meet in a butterfly. Blocks with nothing to join wait for k_attn_decode too: the kernel
+// after this one waits for this one alone. Bound by latency: its blocks find their boundary while
 // k_attn_decode runs, and joining in k_attn_decode instead (the last block to arrive joins an item) took
 // 9.5 us against 7.5 for one sequence of 1003 places, and with one key head over 131072 places, whose
 // parts then all fall to one block, 211 against 27.
@@ -681,9 +682,16 @@ __global__ void __launch_bounds__(kThreads) k_attn_join(const DecodeParams p) {
   Units<C::kTile> un;
   un.count(p);
   const int c = (int)blockIdx.x + 1;
-  if (c >= un.grid) return;
-  const Cursor cur = un.find(p, un.start(c));
-  if (cur.tile == 0 || cur.tile == cur.s.n) return;  // between two items
+  Cursor cur;
+  bool inside = c < un.grid;
+  if (inside) {
+    cur = un.find(p, un.start(c));
+    inside = cur.tile != 0 && cur.tile != cur.s.n;  // else between two items
+  }
+  if (!inside) {
+    pdl_wait_then_release();
+    return;
+  }
   const int64_t item0 = cur.first + (int64_t)cur.hr * (cur.s.n + 1);
   const int c0 = un.block_of(item0), c1 = un.block_of(item0 + cur.s.n - 1);
   const int h = cur.hr / p.rt, row0 = (cur.hr - h * p.rt) * kDecodeRows;

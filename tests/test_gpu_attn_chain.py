@@ -1,0 +1,45 @@
+"""Steps of the attention layer launched one behind the other, without a wait in between, give what
+they give one at a time."""
+import pytest
+import torch
+
+import routed_expert_ffn_moe_gb300 as moe
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    from routed_expert_ffn_moe_gb300 import build
+    build.build()
+    moe.load()
+
+
+@pytest.mark.parametrize("B", [1, 3, 16])
+@pytest.mark.parametrize("kv,D", [("bf16", 128), ("fp8", 64)])
+def test_short_decode_steps_in_a_row(B, kv, D):
+    """Sequences of one tile: no item spans blocks, so k_attn_join has nothing to do, while the step
+    behind it overwrites the queries, the cache and the output."""
+    Hq, Hkv, steps = 8, 2, 60
+    torch.manual_seed(3)
+    qkv = torch.randn(steps, B, (Hq + 2 * Hkv) * D, device="cuda").to(torch.bfloat16)
+    table = torch.randperm(4 * B, device="cuda").to(torch.int32).view(B, 4)
+    lens = [(torch.arange(B, device="cuda") % 4 + n + 1).clamp(max=60).to(torch.int32)
+            for n in range(steps)]
+
+    def run(wait):
+        layer = moe.AttnLayer(Hq, Hkv, D, num_pages=4 * B, max_pages=4, max_batch=B, max_tokens=B,
+                              kv_dtype=kv)
+        out = torch.empty(steps, B, Hq * D, dtype=torch.bfloat16, device="cuda")
+        for n in range(steps):
+            out[n].copy_(layer.forward(qkv[n], table, lens[n]))
+            # once more, with the next step right behind it: no copy in between
+            layer.forward(qkv[n], table, lens[n])
+            if wait:
+                torch.cuda.synchronize()
+        layer.check()
+        return out, layer.k_cache, layer.v_cache
+
+    one, row = run(True), run(False)
+    for a, b in zip(one, row):
+        assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
