@@ -961,6 +961,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
     }
+    // The last product's arrival, which no tile follows that could wait for it to raise the maximum:
+    // here before the block may leave.
+    if (ok && n) drain_bar(&o_full[i], (n - 1) & 1, p.status);
   }
 
   tc_fence_before();

@@ -43,3 +43,35 @@ def test_short_decode_steps_in_a_row(B, kv, D):
     one, row = run(True), run(False)
     for a, b in zip(one, row):
         assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_prefill_calls_in_a_row(D):
+    """Blocks of one call make room for the next one's while their last products end: the same bits as
+    one call at a time."""
+    from attn_helpers import Step, workspace
+
+    steps = [Step(lens=[n], new=[m], Hq=8, Hkv=2, D=D, page=64, seed=n)
+             for n, m in ((1, 1), (70, 70), (300, 5), (5000, 3), (900, 700))]
+    calls = []
+    for s in steps:
+        t, shape = s.device(), s.shape()
+        o = torch.empty(s.T, 8, D, dtype=torch.bfloat16, device="cuda")
+        lse = torch.empty(s.T, 8, device="cuda")
+        ws = workspace(shape, True)
+        calls.append((o, lse, ws, lambda t=t, sh=shape, o=o, lse=lse, ws=ws: moe.moe_attn_prefill(
+            sh, t["q"], t["k"], t["v"], None, None, t["table"], t["lens"], t["q_start"], o, lse, ws)))
+    one = []
+    for o, lse, _, call in calls:
+        call()
+        torch.cuda.synchronize()
+        one.append((o.clone(), lse.clone()))
+        o.fill_(float("nan"))
+    for _ in range(100):
+        for c in calls:
+            c[3]()
+    torch.cuda.synchronize()
+    for (o, lse, ws, _), (o1, lse1) in zip(calls, one):
+        moe.moe_check_device_status(ws)
+        assert torch.equal(o.view(torch.int16), o1.view(torch.int16))
+        assert torch.equal(lse, lse1)
