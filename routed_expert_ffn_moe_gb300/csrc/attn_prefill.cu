@@ -400,7 +400,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   // Phases: q_full, q_empty once a unit; tail_full once a unit that has a tail; o_done, o_free once a
   // unit of which the row tile sees anything; the others once a tile.
   // q_full, full, p_full and o_free are waited on in the pair's even block.
-  __shared__ uint64_t q_full, q_empty, s_full[2][2], p_full[2][2], o_full[2], o_done[2], o_free[2],
+  __shared__ uint64_t q_full, q_empty, s_full[2][2], p_full[2][2], o_full[2][2], o_done[2], o_free[2],
       tail_full, full[2][C::kSlots], empty[2][C::kSlots];  // of K, of V
   __shared__ uint32_t tmem_holder;
   __shared__ int abort_flag_s;
@@ -413,11 +413,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(&q_full, 1);
     mbar_init(&q_empty, 2);                           // both row tiles' MMAs have read it
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&o_full[i], 1);                       // a phase for every PV
-      mbar_init(&o_done[i], 1);                       // the last one
+      mbar_init(&o_done[i], 1);                       // the last PV
       mbar_init(&o_free[i], 4 * C::kBlocks);          // the row tile's warps
       for (int b = 0; b < 2; ++b) {
         mbar_init(&s_full[i][b], 1);
+        mbar_init(&o_full[i][b], 1);                  // a phase for every second PV
         mbar_init(&p_full[i][b], 4 * C::kBlocks);
       }
     }
@@ -734,7 +734,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               begun = true;
             }
             if (ahead) qk(j + 2);
-            if (pv) commit(&o_full[i]);
+            if (pv) commit(&o_full[i][(n_pv & 1) ^ 1]);
             if (j == rt.last) commit(&o_done[i]);
             commit(&empty[1][vs]);
             if (++vs == C::kSlots) { vs = 0; vp ^= 1u; }
@@ -817,8 +817,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (raise) m = mx;
           l *= f;
           if (begun) {
-            ok = wait_bar(&o_full[i], (n - 1) & 1, abort_flag, p.status);  // PV of the tile before
-            // (S of this tile came after the PV before that one: the phase is unambiguous)
+            // PV of the tile before. When S(n) is there, the arrival of PV(n-2), committed right after
+            // it, may still be on its way, so barriers alternate: in one for all, the phase of PV(n-1)
+            // has the parity of PV(n-3)'s and would pass for done.
+            ok = wait_bar(&o_full[i][(n - 1) & 1], ((n - 1) >> 1) & 1, abort_flag, p.status);
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
             tc_fence_after();
@@ -961,9 +963,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
     }
-    // The last product's arrival, which no tile follows that could wait for it to raise the maximum:
+    // The last products' arrivals, which no tile follows that could wait for them to raise the maximum:
     // here before the block may leave.
-    if (ok && n) drain_bar(&o_full[i], (n - 1) & 1, p.status);
+    if (ok && n > 1) drain_bar(&o_full[i][n & 1], ((n - 2) >> 1) & 1, p.status);
+    if (ok && n) drain_bar(&o_full[i][(n - 1) & 1], ((n - 1) >> 1) & 1, p.status);
   }
 
   tc_fence_before();

@@ -171,3 +171,22 @@ def test_one_token_a_sequence_agrees_with_decode():
     _, _, tol, ltol = step.reference(P_ROUND)
     assert ((o.cpu().to(F64) - d_o.cpu().to(F64)).abs() <= 2 * tol).all()
     assert ((lse.cpu().to(F64) - d_lse.cpu().to(F64)).abs() <= 2 * ltol).all()
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_every_tile_raises_the_maximum(D):
+    """Keys that grow by more than the slack of the running maximum from tile to tile: every tile
+    rescales the output, right behind the product of the tile before."""
+    step = Step(lens=[4096, 700], new=[512, 700], Hq=8, Hkv=2, D=D, page=64)
+    step.q = torch.ones_like(step.q)
+    for b, n in enumerate(step.lens):
+        for i in range(-(-n // 64)):
+            m = min(64, n - 64 * i)
+            # scores 16 i at the scale 1/sqrt(D): 2^23 from one tile to the next
+            step.k_view[int(step.table[b, i])][:, :m] = 16 * i / D ** 0.5
+    o, lse = run(step)
+    check_attention(step, o, lse, "every tile", P_ROUND)
+    for _ in range(20):
+        again = run(step)
+        assert torch.equal(o.view(torch.int16), again[0].view(torch.int16))
+        assert torch.equal(lse, again[1])
