@@ -137,10 +137,10 @@ __device__ __forceinline__ uint64_t add_f32x2(uint64_t a, uint64_t b) {
 // A unit is two row tiles of one sequence and key head (in a pair, two of 256 rows): `unit_tok`
 // tokens. All units in a row (sequence, key head, tokens ascending), each weighed by the places
 // that its last token sees plus kUnitCost for its start and end, are cut into equal runs, one per
-// block (pair) of a grid that fills the SMs. A run may begin and end inside a unit, whose parts
-// k_attn_prefill_join then joins; cuts that would leave less than kMinPart key tiles on a side,
-// or that fall into a unit of less than `min_split`, move to the unit's nearer end. A cut costs about
-// 10 us in all, a tile 0.7 us: where there are units enough for every run, units of less than 48
+// block (pair) of a grid that fills the SMs, but of a tile at least. A run may begin and end inside a
+// unit, whose parts k_attn_prefill_join then joins; cuts that would leave less than kMinPart key tiles
+// on a side, or that fall into a unit of less than `min_split`, move to the unit's nearer end. A cut
+// costs about 10 us in all, a tile 0.7 us: where there are units enough for every run, units of less than 48
 // tiles stay whole, else of less than 16. Cut against whole, us: 1024 units of 18 tiles 129 against
 // 122; 8 prompts of 1024 tokens (512 units of up to 17) 158 against 141; 256 units of up to 345, 828
 // against 948. With few units: 16 tokens over 8192 places 32 against 79, over 2048 23 against 26;
@@ -261,7 +261,10 @@ __device__ __forceinline__ Cut find_cut(const PrefillParams& p, int unit_tok, in
 #pragma unroll
   for (int o = 16; o; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
   total *= p.Hkv;
-  const int64_t each = div_s(total, runs), more = total - each * runs;
+  // A run is a tile at least, so that no two cuts of a unit fall on the same step: the join takes a
+  // part from every run between a unit's first and last cut. Runs past the end take nothing.
+  const int64_t shared = max(total, (int64_t)runs * kKeys);
+  const int64_t each = div_s(shared, runs), more = shared - each * runs;
   int64_t x = c * each + min((int64_t)c, more);
   const int64_t here = x;
   Cut cut;

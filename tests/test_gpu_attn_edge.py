@@ -1,0 +1,81 @@
+"""Attention on the GPU where a result could be lost: workspaces with what other calls left there,
+rows whose scores are NaN, probabilities far below the largest, infinite elements, limits beyond
+every place."""
+import pytest
+import torch
+
+import routed_expert_ffn_moe_gb300 as moe
+from attn_helpers import Step, check_attention, workspace
+
+pytestmark = pytest.mark.gpu
+
+P_ROUND = 2.0 ** -8  # prefill: probabilities as one bf16 term
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    from routed_expert_ffn_moe_gb300 import build
+    build.build()
+    moe.load()
+
+
+def run_prefill(step, ws=None, **more):
+    t, s = step.device(), step.shape(**more)
+    ws = workspace(s, True) if ws is None else ws
+    o = torch.full((step.T, step.Hq, step.D), float("nan"), dtype=torch.bfloat16, device="cuda")
+    lse = torch.full((step.T, step.Hq), float("nan"), device="cuda")
+    moe.moe_attn_prefill(s, t["q"], t["k"], t["v"], t["ks"], t["vs"], t["table"], t["lens"],
+                         t["q_start"], o, lse, ws)
+    moe.moe_check_device_status(ws)
+    return o, lse
+
+
+def run_decode(step, ws=None, **more):
+    t, s = step.device(), step.shape(**more)
+    ws = workspace(s) if ws is None else ws
+    o = torch.full((step.T, step.Hq, step.D), float("nan"), dtype=torch.bfloat16, device="cuda")
+    lse = torch.full((step.T, step.Hq), float("nan"), device="cuda")
+    moe.moe_attn_decode(s, t["q"], t["k"], t["v"], t["ks"], t["vs"], t["table"], t["lens"], o, lse,
+                        ws)
+    moe.moe_check_device_status(ws)
+    return o, lse
+
+
+# ---- the workspace holds what other calls left there -------------------------------------------
+
+LEFT = [
+    # few rows over a middling length: less than a tile for each run of the grid
+    dict(lens=[1100], new=[1], Hq=8, Hkv=1),
+    dict(lens=[1100], new=[1], Hq=8, Hkv=1, D=64),
+    dict(lens=[4000], new=[2], Hq=8, Hkv=1),
+    dict(lens=[9000], new=[3], Hq=4, Hkv=1, D=64),
+    dict(lens=[2000, 1500], new=[1, 40], Hq=2, Hkv=1, D=64, page=64),
+    dict(lens=[2000], new=[1], Hq=8, Hkv=1, D=64, kv="fp8"),
+    dict(lens=[3000], new=[5], Hq=8, Hkv=1, D=64, window=1500, sink=100),
+    dict(lens=[20011], new=[70], Hq=4, Hkv=1),
+    # unpacked first, parts of the rows not needed
+    dict(lens=[300, 0, 900, 70], new=[20, 0, 100, 70], Hq=4, Hkv=2, kv="fp8", page=7, window=60, sink=9),
+    dict(lens=[300, 900], new=[200, 3], Hq=4, Hkv=2, D=64, page=24, window=200, sink=130),
+]
+
+
+@pytest.mark.parametrize("kw", LEFT, ids=str)
+@pytest.mark.parametrize("left", [float("nan"), 3.0])
+def test_prefill_takes_nothing_from_the_workspace(kw, left):
+    step = Step(**kw)
+    s = step.shape()
+    ws = workspace(s, True)
+    ws[moe.moe_attn_workspace_zero_bytes():].view(torch.float32).fill_(left)
+    o, lse = run_prefill(step, ws)
+    check_attention(step, o, lse, str(kw), P_ROUND)
+
+
+@pytest.mark.parametrize("kw", LEFT, ids=str)
+@pytest.mark.parametrize("left", [float("nan"), 3.0])
+def test_decode_takes_nothing_from_the_workspace(kw, left):
+    step = Step(**dict(kw, new=[1] * len(kw["lens"])))
+    s = step.shape()
+    ws = workspace(s)
+    ws[moe.moe_attn_workspace_zero_bytes():].view(torch.float32).fill_(left)
+    o, lse = run_decode(step, ws)
+    check_attention(step, o, lse, str(kw))
