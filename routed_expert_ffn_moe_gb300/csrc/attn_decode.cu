@@ -45,6 +45,10 @@ using namespace ptx;
 
 constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
+// The maximum that a warp or a part publishes where no score was above -inf. Finite, so that its factor
+// is 0 or 1 and never a NaN: whether a row saw anything is told by its sum, which is a NaN where a
+// score was (no maximum holds a NaN).
+constexpr float kNoMax = -3e38f;
 
 struct DecodeParams {
   AttnDims a;
@@ -584,7 +588,7 @@ __global__ void __launch_bounds__(kThreads, C::kBlocks) k_attn_decode(const Deco
       for (int i = 0; i < 2; ++i) {
         l[i] += __shfl_xor_sync(0xffffffffu, l[i], 1);
         l[i] += __shfl_xor_sync(0xffffffffu, l[i], 2);
-        const float base = m[i] == -INFINITY ? -INFINITY : m[i] * sc2[i];
+        const float base = m[i] == -INFINITY ? kNoMax : m[i] * sc2[i];
         if (c4 == 0) sml[warp][g + 8 * i] = make_float2(base, l[i]);
       }
       float* mine = reinterpret_cast<float*>(ring + st * C::kStageBytes);
@@ -614,25 +618,22 @@ __global__ void __launch_bounds__(kThreads, C::kBlocks) k_attn_decode(const Deco
       const int64_t head0 = (int64_t)h * a.G + row0;
       for (int task = (int)threadIdx.x; task < rows * (D / 8); task += kThreads) {
         const int r = task / (D / 8), col = (task % (D / 8)) * 8;
-        float mm = -INFINITY;
+        float mm = kNoMax;
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) mm = fmaxf(mm, sml[w][r].x);
         float y[8] = {0, 0, 0, 0, 0, 0, 0, 0}, sum = 0.f;
-        if (mm != -INFINITY) {
 #pragma unroll
-          for (int w = 0; w < kWarps; ++w) {
-            const float f = ex2(sml[w][r].x - mm);
-            sum += f * sml[w][r].y;
-            const float* src = reinterpret_cast<const float*>(
-                smem + w * (C::kStages * C::kStageBytes) + st * C::kStageBytes);
-            const float4* s4 =
-                reinterpret_cast<const float4*>(src + r * D + (col ^ ((r & 7) << 3)));
-            const float4 lo = s4[0], hi = s4[1];
-            y[0] = fmaf(f, lo.x, y[0]); y[1] = fmaf(f, lo.y, y[1]);
-            y[2] = fmaf(f, lo.z, y[2]); y[3] = fmaf(f, lo.w, y[3]);
-            y[4] = fmaf(f, hi.x, y[4]); y[5] = fmaf(f, hi.y, y[5]);
-            y[6] = fmaf(f, hi.z, y[6]); y[7] = fmaf(f, hi.w, y[7]);
-          }
+        for (int w = 0; w < kWarps; ++w) {
+          const float f = ex2(sml[w][r].x - mm);
+          sum += f * sml[w][r].y;
+          const float* src = reinterpret_cast<const float*>(
+              smem + w * (C::kStages * C::kStageBytes) + st * C::kStageBytes);
+          const float4* s4 = reinterpret_cast<const float4*>(src + r * D + (col ^ ((r & 7) << 3)));
+          const float4 lo = s4[0], hi = s4[1];
+          y[0] = fmaf(f, lo.x, y[0]); y[1] = fmaf(f, lo.y, y[1]);
+          y[2] = fmaf(f, lo.z, y[2]); y[3] = fmaf(f, lo.w, y[3]);
+          y[4] = fmaf(f, hi.x, y[4]); y[5] = fmaf(f, hi.y, y[5]);
+          y[6] = fmaf(f, hi.z, y[6]); y[7] = fmaf(f, hi.w, y[7]);
         }
         if (whole) {
           const float inv = sum > 0.f ? vs / sum : (sum == 0.f ? 0.f : sum);
@@ -707,25 +708,23 @@ __global__ void __launch_bounds__(kThreads) k_attn_join(const DecodeParams p) {
     const int task = first + (int)threadIdx.x / lanes;
     const bool live = task < t1;
     const int r = live ? task / (D / 8) : 0, col = live ? (task % (D / 8)) * 8 : 0;
-    float m = -INFINITY, sum = 0.f, y[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+    float m = kNoMax, sum = 0.f, y[8] = {0, 0, 0, 0, 0, 0, 0, 0};
     for (int part = c0 + mine; live && part <= c1; part += lanes) {
       // the part that began the item is its block's second, the others are their blocks' first
       const int64_t at = (int64_t)(2 * part + (part == c0 ? 1 : 0)) * kDecodeRows + r;
       const float2 ml = __ldcg(p.ml + at);
       const float4* src = reinterpret_cast<const float4*>(p.parts + at * D + col);
       const float4 lo = __ldcg(src), hi = __ldcg(src + 1);
-      if (ml.x != -INFINITY) {
-        const float to = fmaxf(m, ml.x), f = ex2(m - to), g = ex2(ml.x - to);
-        const float z[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
-        sum = sum * f + ml.y * g;
+      const float to = fmaxf(m, ml.x), f = ex2(m - to), g = ex2(ml.x - to);
+      const float z[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+      sum = sum * f + ml.y * g;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) y[e] = fmaf(z[e], g, y[e] * f);
-        m = to;
-      }
+      for (int e = 0; e < 8; ++e) y[e] = fmaf(z[e], g, y[e] * f);
+      m = to;
     }
     float all = m;
     for (int o = lanes / 2; o; o >>= 1) all = fmaxf(all, __shfl_xor_sync(0xffffffffu, all, o));
-    const float f = m == -INFINITY ? 0.f : ex2(m - all);
+    const float f = ex2(m - all);
     sum *= f;
 #pragma unroll
     for (int e = 0; e < 8; ++e) y[e] *= f;

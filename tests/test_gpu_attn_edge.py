@@ -79,3 +79,58 @@ def test_decode_takes_nothing_from_the_workspace(kw, left):
     ws[moe.moe_attn_workspace_zero_bytes():].view(torch.float32).fill_(left)
     o, lse = run_decode(step, ws)
     check_attention(step, o, lse, str(kw))
+
+
+# ---- NaN scores -------------------------------------------------------------------------------
+
+def put_key(step, b, j, value):
+    """Sets the key of place j of sequence b (all heads)."""
+    step.k_view[int(step.table[b, j // step.page]), :, j % step.page] = torch.full(
+        (step.Hkv, step.D), value).to(step.k_view.dtype)
+
+
+@pytest.mark.parametrize("kv", ["bf16", "fp8"])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("what", ["decode", "prefill"])
+def test_nan_in_a_query_makes_its_row_nan_and_no_other(what, D, kv):
+    run = run_decode if what == "decode" else run_prefill
+    kw = dict(lens=[1, 40, 300, 20011], new=[1, 1, 1, 1], Hq=40, Hkv=2, D=D, kv=kv)
+    good = run(Step(**kw))
+    step = Step(**kw)
+    hit = torch.zeros(step.T, step.Hq, dtype=torch.bool)
+    for b, h, d in ((0, 3, 0), (1, 0, D - 1), (2, 39, 17), (3, 21, 5), (3, 2, 40)):
+        step.q[b, h, d] = float("nan")
+        hit[b, h] = True
+    o, lse = (x.cpu() for x in run(step))
+    assert torch.isnan(o[hit]).all() and torch.isnan(lse[hit]).all()
+    assert torch.equal(o[~hit].view(torch.int16), good[0].cpu()[~hit].view(torch.int16))
+    assert torch.equal(lse[~hit], good[1].cpu()[~hit])
+
+
+@pytest.mark.parametrize("kv", ["bf16", "fp8"])
+@pytest.mark.parametrize("what", ["decode", "prefill"])
+def test_nan_keys_make_their_sequence_nan(what, kv):
+    """One place, every place, and every place of a block's part."""
+    run = run_decode if what == "decode" else run_prefill
+    kw = dict(lens=[1, 70, 9000, 9000, 33], new=[1] * 5, Hq=8, Hkv=1, kv=kv)
+    good = run(Step(**kw))
+    step = Step(**kw)
+    for b, places in ((0, [0]), (1, range(70)), (2, range(4000, 5200)), (3, [8999])):
+        for j in places:
+            put_key(step, b, j, float("nan"))
+    o, lse = (x.cpu() for x in run(step))
+    assert torch.isnan(o[:4]).all() and torch.isnan(lse[:4]).all()
+    assert torch.equal(o[4].view(torch.int16), good[0][4].cpu().view(torch.int16))
+    assert torch.equal(lse[4], good[1][4].cpu())
+
+
+@pytest.mark.parametrize("kv", ["bf16", "fp8"])
+def test_scores_of_minus_infinity_count_as_not_seen(kv):
+    """softmax of -inf scores is 0 each, and a row of nothing else has no sum: o = 0, lse = -inf."""
+    step = Step(lens=[50, 50], new=[1, 1], Hq=4, Hkv=1, kv=kv, scales=False)
+    for j in range(50):
+        put_key(step, 0, j, 1.0)
+    step.q[0] = -float("inf")
+    o, lse = (x.cpu() for x in run_decode(step))
+    assert (o[0] == 0).all() and torch.isinf(lse[0]).all() and (lse[0] < 0).all()
+    assert torch.isfinite(o[1]).all()
