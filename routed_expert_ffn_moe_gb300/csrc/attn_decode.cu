@@ -23,7 +23,8 @@
 //
 // Probabilities of a bf16 cache enter the product with v as two bf16 terms (2^-16 relative): the
 // tensor cores have room, and one term alone would be the largest error of the result. Those of an
-// E4M3 cache are one f16 term (2^-12 relative): its codes carry 2^-4 themselves.
+// E4M3 cache are one f16 term (2^-12 relative down to 2^-28 of the largest, 2^-39 of that below):
+// its codes carry 2^-4 themselves.
 //
 // E4M3 codes enter the MMAs as f16 (exactly). The queries become f16 too, each row times the
 // power of two that brings its largest element to [2^14, 2^15), taken back in the scores'
@@ -130,6 +131,9 @@ template <int D_, bool FP8_>
 struct Cfg {
   static constexpr int D = D_;
   static constexpr bool FP8 = FP8_;
+  // Exponents are formed this much higher where probabilities are f16: the largest becomes 2^14, and
+  // what is below 2^-39 of it, not 2^-25, is lost (of one key; a block may hold 10^5 of them).
+  static constexpr float kUp = FP8 ? 14.f : 0.f;
   static constexpr int kRowBytes = FP8 ? D : 2 * D;
   static constexpr int kKeys = 4096 / kRowBytes;       // keys of a warp in a tile: 8 KB with values
   static constexpr int kTile = kKeys * kWarps;         // keys of a unit
@@ -504,13 +508,16 @@ __global__ void __launch_bounds__(kThreads, C::kBlocks) k_attn_decode(const Deco
         mx[i] = fmaxf(mx[i], __shfl_xor_sync(0xffffffffu, mx[i], 1));
         mx[i] = fmaxf(mx[i], __shfl_xor_sync(0xffffffffu, mx[i], 2));
       }
-      float base[2];
+      float top[2], base[2];
 #pragma unroll
-      for (int i = 0; i < 2; ++i) base[i] = mx[i] == -INFINITY ? 0.f : mx[i] * sc2[i];
+      for (int i = 0; i < 2; ++i) {
+        top[i] = mx[i] == -INFINITY ? 0.f : mx[i] * sc2[i];
+        base[i] = top[i] - C::kUp;
+      }
       if (__any_sync(0xffffffffu, mx[0] > m[0] || mx[1] > m[1])) {
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          const float f = m[i] == -INFINITY ? 0.f : ex2(fmaf(m[i], sc2[i], -base[i]));
+          const float f = m[i] == -INFINITY ? 0.f : ex2(fmaf(m[i], sc2[i], -top[i]));
           l[i] *= f;
 #pragma unroll
           for (int n = 0; n < NT; ++n) {
@@ -588,7 +595,7 @@ __global__ void __launch_bounds__(kThreads, C::kBlocks) k_attn_decode(const Deco
       for (int i = 0; i < 2; ++i) {
         l[i] += __shfl_xor_sync(0xffffffffu, l[i], 1);
         l[i] += __shfl_xor_sync(0xffffffffu, l[i], 2);
-        const float base = m[i] == -INFINITY ? kNoMax : m[i] * sc2[i];
+        const float base = m[i] == -INFINITY ? kNoMax : m[i] * sc2[i] - C::kUp;
         if (c4 == 0) sml[warp][g + 8 * i] = make_float2(base, l[i]);
       }
       float* mine = reinterpret_cast<float*>(ring + st * C::kStageBytes);

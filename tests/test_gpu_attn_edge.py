@@ -5,7 +5,7 @@ import pytest
 import torch
 
 import routed_expert_ffn_moe_gb300 as moe
-from attn_helpers import Step, check_attention, workspace
+from attn_helpers import F64, Step, check_attention, workspace
 
 pytestmark = pytest.mark.gpu
 
@@ -134,3 +134,33 @@ def test_scores_of_minus_infinity_count_as_not_seen(kv):
     o, lse = (x.cpu() for x in run_decode(step))
     assert (o[0] == 0).all() and torch.isinf(lse[0]).all() and (lse[0] < 0).all()
     assert torch.isfinite(o[1]).all()
+
+
+# ---- probabilities far below the largest --------------------------------------------------------
+
+@pytest.mark.parametrize("lens,D", [([600], 128), ([600], 64), ([20000], 128)])
+@pytest.mark.parametrize("below", [10, 14, 18, 22, 26, 30, 36])
+@pytest.mark.parametrize("kv", ["bf16", "fp8"])
+def test_decode_keeps_small_probabilities(kv, below, lens, D):
+    """One key whose value is zero takes nearly all of the softmax; the output is what the others add,
+    each about 2^-below of it. Over E4M3 a probability is an f16 times 2^14: half its smallest step is
+    2^-39 of the largest probability, for each of the n keys, beside the relative bound."""
+    step = Step(lens=lens, new=[1], Hq=8, Hkv=1, D=D, kv=kv, scales=False, page=32)
+    step.q = torch.full_like(step.q, 1.0)
+    n = lens[0]
+    big = below * 0.6931471805599453 / D ** 0.5  # times 1: every element of the key, score * scale
+    for i in range(step.max_pages):
+        m = min(32, n - 32 * i)
+        page = int(step.table[0, i])
+        step.k_view[page][:, :m] = torch.zeros(m, D).to(step.k_view.dtype)
+        v = 1 + 0.25 * torch.arange(D) / D
+        step.v_view[page][:, :m] = v.expand(1, m, D).to(step.v_view.dtype)
+    put_key(step, 0, n // 2, big)
+    at = int(step.table[0, (n // 2) // 32])
+    step.v_view[at][:, (n // 2) % 32] = torch.zeros(D).to(step.v_view.dtype)
+    o, lse = run_decode(step)
+    ref, ref_lse, o_tol, lse_tol = step.reference()
+    if kv == "fp8":
+        o_tol = o_tol + n * 2.0 ** -39 * 1.25
+    assert ((o.cpu().to(F64) - ref).abs() <= o_tol).all()
+    assert ((lse.cpu().to(F64) - ref_lse).abs() <= lse_tol).all()
