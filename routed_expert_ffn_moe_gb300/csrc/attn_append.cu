@@ -13,7 +13,8 @@
 // butterfly over those lanes, a pair of neighbours turns inside a lane, and the other half of a
 // pair (i, i + rot/2) is fetched from its lane as packed bf16. With coefficients that a lane forms
 // once per token and kind of head, A = w c and S = +-w' s (w' and s of the other element of the
-// pair), a head is  y = inv (x A + x' S).
+// pair), a head is  y = inv (x A + x' S); where nothing turns x' and S are zeros, so that an
+// infinity passes through (0 times one would be a NaN).
 // A lane group belongs to one token and takes its heads in turn, a batch of loads ahead; it finds
 // its token's sequence, place and page by itself while the first batch is on its way. Nothing
 // synchronises a block.
@@ -173,6 +174,7 @@ __device__ __forceinline__ Place find_place(const AppendParams& p, int tok) {
 struct Turn {
   uint64_t A[4], S[4];
   int partner;
+  uint32_t other;  // ones where the lane's elements turn: a mask of the other halves
 };
 
 template <int LPH>
@@ -181,6 +183,7 @@ __device__ __forceinline__ void coefficients(const AppendParams& p, const Place&
   const AttnDims& a = p.a;
   const int sub = (int)threadIdx.x % LPH, half = a.rot_dim >> 1;
   const bool turns = at.live && sub * 8 < a.rot_dim, first = sub * 8 < half;
+  k.other = turns ? 0xffffffffu : 0u;
   k.partner = !turns || a.rot_pairs ? sub : first ? sub + (half >> 3) : sub - (half >> 3);
   float own[8], other[8];
 #pragma unroll
@@ -192,7 +195,7 @@ __device__ __forceinline__ void coefficients(const AppendParams& p, const Place&
 #pragma unroll
   for (int e = 0; e < 4; ++e) {
     k.A[e] = pair_of(own[2 * e], own[2 * e + 1]);
-    k.S[e] = 0;
+    k.S[e] = pair_of(-0.f, -0.f);  // x A + 0 S is x A of either sign
   }
   if (!turns) return;
   const float* cs = p.cos_sin + (int64_t)at.pos * a.rot_dim +
@@ -224,9 +227,10 @@ __device__ __forceinline__ void turn_head(const AttnDims& a, const Turn& k, bool
   for (int e = 0; e < 4; ++e) {
     x[e] = pair_of(bf16_lo(in[e]), bf16_hi(in[e]));
     if (a.rot_pairs) {
-      y[e] = pair_of(bf16_hi(in[e]), bf16_lo(in[e]));
+      const uint32_t o = in[e] & k.other;
+      y[e] = pair_of(bf16_hi(o), bf16_lo(o));
     } else {
-      const uint32_t o = __shfl_sync(0xffffffffu, in[e], lane0 + k.partner);
+      const uint32_t o = __shfl_sync(0xffffffffu, in[e], lane0 + k.partner) & k.other;
       y[e] = pair_of(bf16_lo(o), bf16_hi(o));
     }
   }

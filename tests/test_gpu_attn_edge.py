@@ -164,3 +164,49 @@ def test_decode_keeps_small_probabilities(kv, below, lens, D):
         o_tol = o_tol + n * 2.0 ** -39 * 1.25
     assert ((o.cpu().to(F64) - ref).abs() <= o_tol).all()
     assert ((lse.cpu().to(F64) - ref_lse).abs() <= lse_tol).all()
+
+
+# ---- append: what does not turn is copied -------------------------------------------------------
+
+@pytest.mark.parametrize("T", [3, 5000])     # the small kernel, the large one
+@pytest.mark.parametrize("rot,pairs", [(0, False), (32, False), (32, True)])
+@pytest.mark.parametrize("D,kv", [(128, "bf16"), (64, "bf16"), (128, "fp8")])
+def test_append_copies_what_does_not_turn(D, kv, rot, pairs, T):
+    """Heads without a norm: elements past rot_dim come out as they went in, infinities, NaN and negative
+    zeros among them, and do not touch their neighbours."""
+    Hq, Hkv = 6, 2
+    step = Step(lens=[T], new=[T], Hq=Hq, Hkv=Hkv, D=D, kv=kv, scales=False)
+    t = step.device()
+    g = torch.Generator().manual_seed(5)
+    qkv = torch.randn(T, Hq + 2 * Hkv, D, generator=g).to(torch.bfloat16)
+    odd = torch.tensor([float("inf"), -float("inf"), float("nan"), -0.0, 3e38]).to(torch.bfloat16)
+    for n in range(40):
+        h = int(torch.randint(Hq + 2 * Hkv, (1,), generator=g))
+        d = int(torch.randint(rot, D, (1,), generator=g))
+        qkv[int(torch.randint(T, (1,), generator=g)), h, d] = odd[n % 5]
+    ang = torch.rand(T, max(rot // 2, 1), generator=g) * 6
+    cs = torch.cat([ang.cos(), ang.sin()], 1)
+    row = (Hq + 2 * Hkv) * D
+    s = step.shape(rot_dim=rot, rot_pairs=pairs, max_pos=T, q_stride=row, k_stride=row, v_stride=row)
+    dev, ws = qkv.cuda().view(T, row), workspace(s)
+    out = torch.empty(T, Hq, D, dtype=torch.bfloat16, device="cuda")
+    moe.moe_attn_append(s, dev, dev[:, Hq * D:], dev[:, (Hq + Hkv) * D:], None, None,
+                        cs.cuda() if rot else None, None, t["table"], t["lens"], t["q_start"], None,
+                        None, out, t["k"], t["v"], ws)
+    moe.moe_check_device_status(ws)
+
+    def same(a, b):
+        nan = torch.isnan(a.float())
+        assert torch.equal(nan, torch.isnan(b.float()))
+        a, b = a.masked_fill(nan, 0), b.masked_fill(nan, 0)
+        assert torch.equal(a.view(torch.int16), b.view(torch.int16))
+
+    same(out.cpu()[..., rot:], qkv[:, :Hq, rot:])
+    j = torch.arange(T)
+    for name, h0, e0 in (("k", Hq, rot), ("v", Hq + Hkv, 0)):
+        got = t[name].float().cpu()[step.table[0, j // step.page].long(), :, j % step.page]
+        want = qkv[:, h0:h0 + Hkv]
+        if kv == "fp8":  # saturating
+            want = want.float().clamp(-448, 448).to(torch.float8_e4m3fn).float().to(torch.bfloat16)
+        same(got.to(torch.bfloat16)[..., e0:], want[..., e0:])
+    assert torch.isfinite(out[..., :rot]).all()
