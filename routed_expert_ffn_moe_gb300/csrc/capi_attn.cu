@@ -1,4 +1,5 @@
 // The C ABI of the attention operators (include/moe.h): host-side validation and dispatch.
+#include <algorithm>
 #include <cmath>
 
 #include "attn.h"
@@ -53,8 +54,10 @@ moe_status check_attn(const moe_attn_shape* s, AttnDims* a) {
   a->page_size = s->page_size;
   a->max_pages = s->max_pages;
   a->num_pages = s->num_pages;
-  a->window = s->window;
-  a->n_sink = s->window ? s->n_sink : 0;
+  // no place lies beyond those of the table, and sums with limits up to 2^30 fit 32 bits
+  const int places = s->page_size * s->max_pages;
+  a->window = std::min(s->window, places);
+  a->n_sink = s->window ? std::min(s->n_sink, places) : 0;
   a->rot_dim = s->rot_dim;
   a->rot_pairs = s->rot_pairs != 0;
   a->max_pos = s->max_pos;

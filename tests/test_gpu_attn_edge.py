@@ -210,3 +210,28 @@ def test_append_copies_what_does_not_turn(D, kv, rot, pairs, T):
             want = want.float().clamp(-448, 448).to(torch.float8_e4m3fn).float().to(torch.bfloat16)
         same(got.to(torch.bfloat16)[..., e0:], want[..., e0:])
     assert torch.isfinite(out[..., :rot]).all()
+
+
+# ---- limits beyond every place ------------------------------------------------------------------
+
+MOST = 2 ** 31 - 1
+
+
+@pytest.mark.parametrize("more", [
+    dict(window=MOST, n_sink=0),
+    dict(window=MOST, n_sink=MOST),
+    dict(window=64, n_sink=MOST),
+    dict(window=MOST - 40, n_sink=3),
+], ids=["window", "both", "sinks", "nearly"])
+@pytest.mark.parametrize("kw", [
+    dict(lens=[10, 300, 700], new=[25, 280, 3], Hq=8, Hkv=2),             # 15 rows of padding
+    dict(lens=[10, 300, 700], new=[25, 280, 3], Hq=8, Hkv=2, D=64, kv="fp8", page=24),
+    dict(lens=[4000], new=[200], Hq=8, Hkv=2, page=64),
+], ids=["bf16", "fp8", "long"])
+def test_limits_beyond_every_place_are_none(kw, more):
+    plain, step = Step(**kw), Step(**kw)
+    o, lse = run_prefill(step, **more)
+    check_attention(plain, o, lse, "prefill", P_ROUND)
+    one = dict(kw, new=[1] * len(kw["lens"]))
+    o, lse = run_decode(Step(**one), **more)
+    check_attention(Step(**one), o, lse, "decode")
