@@ -321,7 +321,8 @@ MOE_API moe_status moe_attn_decode(const moe_attn_shape* shape, const void* q,
  * or more tokens, 64 places) that do not see it. Beyond kv_len, and in pages that no token of
  * the step sees anything of, it does not. E4M3 caches, and bf16 caches whose pages are not a
  * multiple of 16 tokens, are first unpacked into the workspace
- * (4 B Hkv max_pages page_size D bytes, max_pages page_size rounded up to 128). */
+ * (4 B Hkv max_pages page_size D bytes, max_pages page_size rounded up to 128, at most 2^40): the
+ * tables' width counts, not the lengths. */
 MOE_API moe_status moe_attn_prefill(const moe_attn_shape* shape, const void* q,
                                     const void* k_cache, const void* v_cache,
                                     const float* k_scale, const float* v_scale,

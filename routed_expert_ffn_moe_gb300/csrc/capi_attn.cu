@@ -85,6 +85,16 @@ moe_status check_attn(const moe_attn_shape* s, AttnDims* a) {
                      kv * s->page_size, esz, &a->page_stride);
 }
 
+// the rows that prefill unpacks a cache into: within what a size and a tensor map's strides hold
+moe_status check_unpacked(const AttnDims& a) {
+  const int64_t row = (int64_t)a.B * a.Hkv * a.D * 4;  // bytes of a place, keys and values
+  if (!prefill_reads_pages(a) && row && unpacked_len(a) > ((int64_t)1 << 40) / row)
+    return fail(MOE_ERR_INVALID_ARG,
+                "B=%d sequences of %lld places, unpacked for prefill, are over 2^40 bytes", a.B,
+                (long long)unpacked_len(a));
+  return MOE_OK;
+}
+
 moe_status check_attn_ws(const AttnDims& a, int prefill, const void* ws, size_t ws_bytes,
                          AttnWs* L) {
   REQUIRE_PTR(ws, 256);
@@ -112,6 +122,7 @@ extern "C" {
 size_t moe_attn_workspace_size(const moe_attn_shape* shape, int prefill) {
   AttnDims a;
   if (check_attn(shape, &a) != MOE_OK) return 0;
+  if (prefill && check_unpacked(a) != MOE_OK) return 0;
   return attn_ws(a, prefill).total;
 }
 
@@ -194,6 +205,7 @@ moe_status moe_attn_prefill(const moe_attn_shape* shape, const void* q, const vo
   if (st != MOE_OK) return st;
   if ((int64_t)a.T * a.Hkv >= (int64_t)1 << 30)
     return fail(MOE_ERR_INVALID_ARG, "T=%d times Hkv=%d is over 2^30", a.T, a.Hkv);
+  if ((st = check_unpacked(a)) != MOE_OK) return st;
   AttnWs L;
   if ((st = check_attn_ws(a, 1, ws, ws_bytes, &L)) != MOE_OK) return st;
   if (a.T == 0 || a.B == 0) return MOE_OK;
