@@ -379,8 +379,11 @@ class AttnLayer:
     [(Hq + 2 Hkv) * D] bf16 a token (query heads, key heads, value heads), appends keys and values
     to the cache and returns o [T, Hq * D] bf16: attention of one token a sequence where q_start is
     None, else of the ragged step that q_start [B + 1] describes. kv_len [B] counts the step's
-    tokens; block_table [B, max_pages] names each sequence's pages. All three are int32 CUDA
-    tensors. Out-of-range pages, lengths and positions are reported by `check()`.
+    tokens; block_table [B, max_pages] names each sequence's pages. All three are int32, packed, on the
+    layer's device; the rows of qkv may lie apart. Tensors of another type or layout raise ValueError;
+    out-of-range pages, lengths and positions are reported by `check()`. o is the layer's own buffer:
+    the next forward overwrites it. Optional: positions [T] int32 (of the rotation), lse [T, Hq] fp32
+    (written).
 
     max_batch and max_tokens bound the sequences and tokens of a step. norms: (q_norm, k_norm), [D]
     bf16 each, or None; scales: (k_scale, v_scale), [Hkv] fp32 each, for an "fp8" cache.
@@ -396,16 +399,24 @@ class AttnLayer:
         self.max_batch, self.max_tokens, self.max_pages = max_batch, max_tokens, max_pages
         self.q_norm, self.k_norm = norms or (None, None)
         self.k_scale, self.v_scale = scales or (None, None)
+        self._i32, self._bf16, self._f32 = torch.int32, torch.bfloat16, torch.float32
         rot_dim = D if rot_dim is None else rot_dim
         max_pos = page_size * max_pages
         self._kw = dict(Hq=Hq, Hkv=Hkv, D=D, kv_dtype=kv_dtype, page_size=page_size,
                         max_pages=max_pages, num_pages=num_pages, window=window, n_sink=n_sink,
                         rot_dim=rot_dim, rot_pairs=rot_pairs, max_pos=max_pos, scale=scale,
-                        eps=eps, q_stride=row, k_stride=row, v_stride=row)
+                        eps=eps)
+        self._row = row
         dev = torch.device(device)
         dt = torch.bfloat16 if kv_dtype == "bf16" else torch.uint8
         self.k_cache = torch.zeros(num_pages, Hkv, page_size, D, dtype=dt, device=dev)
         self.v_cache = torch.zeros_like(self.k_cache)
+        self._dev = self.k_cache.device
+        for name, t, kind, n in (("q_norm", self.q_norm, self._bf16, D),
+                                 ("k_norm", self.k_norm, self._bf16, D),
+                                 ("k_scale", self.k_scale, self._f32, Hkv),
+                                 ("v_scale", self.v_scale, self._f32, Hkv)):
+            self._packed(name, t, kind, n)
         freq = rope_base ** (-torch.arange(rot_dim // 2, dtype=torch.float64) / max(rot_dim // 2, 1))
         ang = torch.arange(max_pos, dtype=torch.float64)[:, None] * freq
         self.cos_sin = torch.cat([ang.cos(), ang.sin()], 1).float().contiguous().to(dev)
@@ -418,17 +429,43 @@ class AttnLayer:
         self.o = torch.empty(max_tokens, Hq * D, dtype=torch.bfloat16, device=dev)
         self._shapes = {}
 
+    def _packed(self, name, t, dtype, n):
+        """Refuses a tensor whose first n elements do not lie in a row as `dtype` on the device."""
+        if t is None or isinstance(t, int):  # an int is an address
+            return
+        if t.dtype != dtype or t.device != self._dev or t.numel() < n or not t.is_contiguous():
+            raise ValueError(f"{name}: {t.dtype}, {tuple(t.shape)}, strides {t.stride()} on {t.device}: "
+                             f"{n} packed elements of {dtype} on {self._dev} are needed")
+
+    def _rows_apart(self, qkv, T):
+        """The distance of qkv's rows, each (Hq + 2 Hkv) * D bf16 in a row."""
+        row = self._row
+        if qkv.dtype == self._bf16 and qkv.device == self._dev and qkv.numel() == T * row:
+            if qkv.is_contiguous():
+                return row
+            if qkv[0].is_contiguous() and qkv.stride(0) >= row:
+                return qkv.stride(0)
+        raise ValueError(f"qkv: {qkv.dtype}, {tuple(qkv.shape)}, strides {qkv.stride()} on "
+                         f"{qkv.device}: rows of {row} packed bf16 on {self._dev} are needed")
+
     def forward(self, qkv, block_table, kv_len, q_start=None, positions=None, lse=None, stream=None):
         T, B = qkv.shape[0], kv_len.shape[0]
         if T > self.max_tokens or B > self.max_batch or block_table.shape[1] != self.max_pages:
             raise ValueError(f"a step of {T} tokens, {B} sequences and tables of "
                              f"{block_table.shape[1]} pages: the layer was made for "
                              f"{self.max_tokens}, {self.max_batch} and {self.max_pages}")
-        s = self._shapes.get((T, B))
+        apart = self._rows_apart(qkv, T)
+        self._packed("block_table", block_table, self._i32, B * self.max_pages)
+        self._packed("kv_len", kv_len, self._i32, B)
+        self._packed("q_start", q_start, self._i32, B + 1)
+        self._packed("positions", positions, self._i32, T)
+        self._packed("lse", lse, self._f32, T * self.Hq)
+        s = self._shapes.get((T, B, apart))
         if s is None:
             if len(self._shapes) >= 1024:
                 self._shapes.clear()
-            s = self._shapes[(T, B)] = attn_shape(T=T, B=B, **self._kw)
+            s = self._shapes[(T, B, apart)] = attn_shape(T=T, B=B, q_stride=apart, k_stride=apart,
+                                                         v_stride=apart, **self._kw)
         nq, nk = self.Hq * self.D, self.Hkv * self.D
         at = qkv.data_ptr()
         q, k, v = (at, at + 2 * nq, at + 2 * (nq + nk)) if T else (None, None, None)

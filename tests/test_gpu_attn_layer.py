@@ -79,3 +79,26 @@ def test_layer_in_a_cuda_graph():
         again = layer.forward(qkv, table, lens)
         assert torch.equal(got.view(torch.int16), again.view(torch.int16)), n
     layer.check()
+
+
+@pytest.mark.parametrize("kv", ["bf16", "fp8"])
+def test_layer_takes_rows_that_lie_apart(kv):
+    # a projection that has more columns than the layer needs, and arrays made for larger batches
+    torch.manual_seed(4)
+    row, T = 12 * 128, 50
+    wide = torch.randn(T, row + 64, device="cuda").to(torch.bfloat16)
+    table = torch.arange(12, dtype=torch.int32, device="cuda").view(3, 4)
+    lens = torch.tensor([40, 11], dtype=torch.int32, device="cuda")
+    start = torch.tensor([0, 40, 50, 99, 99], dtype=torch.int32, device="cuda")
+    out = []
+    for qkv in (wide[:, :row], wide[:, :row].contiguous(), wide[:, :row].reshape(T, 12, 128)):
+        layer = moe.AttnLayer(8, 2, 128, num_pages=12, max_pages=4, max_batch=4, max_tokens=64,
+                              kv_dtype=kv)
+        lse = torch.zeros(T, 8, device="cuda")
+        o = layer.forward(qkv, table, lens, start, lse=lse)
+        one = layer.forward(qkv[:2], table, lens + 1)
+        layer.check()
+        out.append((o.clone(), one.clone(), lse, layer.k_cache, layer.v_cache))
+    for other in out[1:]:
+        for a, b in zip(out[0], other):
+            assert torch.equal(a.contiguous().view(torch.uint8), b.contiguous().view(torch.uint8))
