@@ -408,7 +408,7 @@ class AttnLayer:
                         eps=eps)
         self._row = row
         dev = torch.device(device)
-        dt = torch.bfloat16 if kv_dtype == "bf16" else torch.uint8
+        dt = torch.bfloat16 if kv_dtype in ("bf16", MOE_KV_BF16) else torch.uint8
         self.k_cache = torch.zeros(num_pages, Hkv, page_size, D, dtype=dt, device=dev)
         self.v_cache = torch.zeros_like(self.k_cache)
         self._dev = self.k_cache.device

@@ -78,3 +78,13 @@ def test_wrong_weights_are_refused(kw, word):
     with pytest.raises(ValueError, match=word):
         moe.AttnLayer(HQ, HKV, D, num_pages=8, max_pages=PAGES, max_batch=4, max_tokens=16,
                       device="cpu", **kw)
+
+
+@pytest.mark.parametrize("name,number,dtype", [("bf16", moe.MOE_KV_BF16, BF16),
+                                               ("fp8", moe.MOE_KV_FP8_E4M3, torch.uint8)])
+def test_the_cache_holds_what_its_type_needs(name, number, dtype):
+    # the type by its name or by the library's number
+    for kv in (name, number):
+        layer = moe.AttnLayer(HQ, HKV, D, num_pages=8, max_pages=PAGES, max_batch=4, max_tokens=16,
+                              kv_dtype=kv, device="cpu")
+        assert layer.k_cache.dtype == dtype and layer.v_cache.dtype == dtype
