@@ -303,8 +303,8 @@ MOE_API moe_status moe_attn_append(const moe_attn_shape* shape, const void* q, c
  *   q [B, Hq, D] bf16, o [B, Hq, D] bf16 out, lse [B, Hq] fp32 out or NULL.
  * A sequence with kv_len = 0 gives o = 0 and lse = -inf. Scores, the softmax's maximum and sum
  * and the output are held in fp32; the probabilities enter the product with v as f16 (E4M3 cache)
- * or as the sum of two bf16 (bf16 cache). The result does not depend on the order in which blocks
- * run. */
+ * or as the sum of two bf16 (bf16 cache). A NaN among the scores that a row sees makes the row NaN.
+ * The result does not depend on the order in which blocks run. */
 MOE_API moe_status moe_attn_decode(const moe_attn_shape* shape, const void* q,
                                    const void* k_cache, const void* v_cache,
                                    const float* k_scale, const float* v_scale,

@@ -386,7 +386,9 @@ class AttnLayer:
     (written).
 
     max_batch and max_tokens bound the sequences and tokens of a step. norms: (q_norm, k_norm), [D]
-    bf16 each, or None; scales: (k_scale, v_scale), [Hkv] fp32 each, for an "fp8" cache.
+    bf16 each, or None; scales: (k_scale, v_scale), [Hkv] fp32 each, for an "fp8" cache. For such a
+    cache, and for pages that are no multiple of 16 tokens, the workspace also holds the bf16 keys and
+    values of max_batch sequences of max_pages * page_size places, unpacked by steps with q_start.
     """
 
     def __init__(self, Hq, Hkv, D, num_pages, page_size=16, max_pages=256, max_batch=64,

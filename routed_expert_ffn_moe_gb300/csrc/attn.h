@@ -56,9 +56,10 @@ constexpr int kPrefillKeys = 128;  // the unpacked rows are made in runs of so m
 // Prefill tiles are read by TMA in boxes of one page each: bf16 pages of a multiple of 16 tokens.
 // Other caches are unpacked first: E4M3 because the products take bf16, odd pages because a box is
 // whole 8-row atoms of the swizzle, and pages of 8 because eight boxes a tile take longer than the
-// tile. 64 heads of 128, in place against unpacked, us: 2048 tokens over 16384, pages of 8 1275
-// against 682, of 16 751 against 699, of 32 680 against 689; 8 prompts of 1500, 390 against 273,
-// 261 against 269, 257 against 278; 16 tokens over 16384, 64 against 68, 45 against 68.
+// tile (2048 tokens over 16384 places of 64 heads of 128, 1275 us in place against 682, 8 prompts of
+// 1500, 390 against 273, both with an earlier tile loop). In place against unpacked now, us, pages of 16
+// and 32: 2048 over 16384, 648 and 648 against 671; 8 x 1500, 241 and 238 against 264; 16 tokens over
+// 16384, 42 and 40 against 67.
 inline bool prefill_reads_pages(const AttnDims& a) { return !a.fp8 && a.page_size % 16 == 0; }
 
 inline int64_t unpacked_len(const AttnDims& a) {

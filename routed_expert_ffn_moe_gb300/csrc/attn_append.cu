@@ -26,9 +26,9 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kBatch = 4;  // heads of a batch
 // Lanes (tokens x heads x D / 8) of a small step. Small kernel against large, us, bf16, query + key
-// heads: of 64, 4+1, 1024 tokens 2.8 against 4.3, 4096 5.3 against 4.7; 64+8, 256 tokens 3.6 against
-// 4.1, 1024 9.6 against 8.6. Of 128, 4+1, 1024 tokens 3.5 against 4.3, 2048 5.4 against 4.7; 64+8, 64
-// tokens 3.0 against 4.8, 256 5.8 against 6.1, 1024 18.7 against 12.4.
+// heads: of 64, 4+1, 1024 tokens 2.6 against 4.2, 4096 4.7 against 4.2; 64+8, 256 tokens 3.4 against
+// 4.2, 1024 9.3 against 8.9. Of 128, 4+1, 1024 tokens 3.5 against 4.3, 2048 4.9 against 4.4; 64+8, 64
+// tokens 2.8 against 4.3, 256 5.7 against 6.3, 1024 20.5 against 14.4.
 constexpr int64_t kSmallLanes = 5 << 16;
 
 struct AppendParams {
@@ -265,7 +265,8 @@ __device__ __forceinline__ void store_cache(const AppendParams& p, uint8_t* cach
 }
 
 // Large steps: a lane group takes the heads of its token in turn, `groups` of them to a token. 16245
-// tokens of 64 + 8 + 8 heads of 128: 106 us, 0.93 of the measured copy rate; 4096, 34 us, 0.73.
+// tokens of 64 + 8 + 8 heads of 128: 107 us, 0.92 of the measured copy rate; 4096, 34 us, 0.73; over
+// E4M3, 16384 tokens 119 us, 0.80.
 template <int D, bool FP8>
 __global__ void __launch_bounds__(kThreads, 3) k_attn_append(const AppendParams p) {
   constexpr int LPH = D / 8, GROUPS = kThreads / LPH;
@@ -382,8 +383,8 @@ cudaError_t launch(AppendParams& p, cudaStream_t st) {
   // Fewer groups a token mean fewer look-ups and more heads a group: no more groups than batches of
   // query heads; 16 query heads a group as long as that fills the SMs' places (three blocks each);
   // and more where the blocks would fill them eight times over. 64 + 8 heads of 128, 4096 tokens,
-  // 16, 8, 4 groups: 38.7, 36.8, 34.0 us; 16384 tokens, 4, 2, 1: 109.8, 107.7, 114.3. 14 + 2 heads of 64,
-  // 4096 tokens, 32, 2: 18.5, 7.7.
+  // 16, 8, 4 groups: 54.0, 38.4, 34.5 us; 16384 tokens, 4, 2, 1: 112.2, 109.2, 115.5. 14 + 2 heads of 64,
+  // 4096 tokens, 32, 2: 35.6, 7.8.
   p.groups = GROUPS;
   const auto blocks = [&] { return (int64_t)p.a.T * p.groups / GROUPS; };
   while (p.groups > 1 && (p.groups * kBatch > p.a.Hq || blocks() > 24 * num_sms() ||

@@ -3,8 +3,8 @@
 //   s_j = scale q.k_j over the visible places j,  o = sum_j e^(s_j - m) v_j / l,
 //   m = max_j s_j,  l = sum_j e^(s_j - m),  lse = m + ln l
 //
-// What bounds it: HBM. Every visible key and value is read once, 2 G multiply-adds an element,
-// far below the tensor cores' rate even padded to 16 query heads.
+// What bounds it: HBM. Every visible key and value is read once for each 16 query heads of its key
+// head, 2 G multiply-adds an element, far below the tensor cores' rate even padded to 16 query heads.
 //
 // Work split. An item is one sequence, one key head and up to 16 of its query heads; a unit is
 // one tile of an item's visible keys (64 of 256 bytes, in general 32 KB of keys and values), or the
@@ -23,7 +23,7 @@
 //
 // Probabilities of a bf16 cache enter the product with v as two bf16 terms (2^-16 relative): the
 // tensor cores have room, and one term alone would be the largest error of the result. Those of an
-// E4M3 cache are one f16 term (2^-12 relative down to 2^-28 of the largest, 2^-39 of that below):
+// E4M3 cache are one f16 term (2^-11 relative down to 2^-28 of the largest, 2^-39 of that below):
 // its codes carry 2^-4 themselves.
 //
 // E4M3 codes enter the MMAs as f16 (exactly). The queries become f16 too, each row times the
@@ -33,9 +33,11 @@
 // and the columns of v (stored back in place).
 //
 // Measured, of a copy rate of 6772 GB/s, 8 key heads of 128, 64 query heads: 256 sequences of 2048
-// to 8192 places, bf16, 798 us, 1.0; one of 131071, 88 us, 0.90, of 524288, 318 us, 1.0; 64 sequences
-// of 2048 places in E4M3 pages of 16, 64 us, 0.63, of 32768, 767 us, 0.83 (runs of 2 KB, the conversions,
-// and the 8 warps that the registers leave an SM); one of 1003 places, 7.2 us: the start of two kernels.
+// to 8192 places, bf16, 812 us, 0.98; one of 131071, 89 us, 0.89, of 524288, 324 us, 0.98; 64 sequences
+// of 2048 places in E4M3 pages of 16, 63 us, 0.63, of 32768, 769 us, 0.83, in pages of 64, 701 us, 0.91
+// (runs of 2 KB, the conversions, and the 8 warps that the registers leave an SM); one of 1003 places, 7.1
+// us: the start of two kernels. Wider groups read again: 64 sequences of 8192 places, one key head of
+// 128, bf16, 16, 32, 64, 128 query heads: 56, 93, 172, 264 us.
 #include "attn.h"
 #include "sm100_ptx.cuh"
 
@@ -144,9 +146,9 @@ struct Cfg {
   // Resident blocks of an SM, which share its registers and shared memory: three of two stages
   // where a warp's fragments fit in 168 registers and the conversions of E4M3 keep it busier than
   // the loads, else two of three. 96 sequences of 2 key heads of 64, E4M3, three against two, us:
-  // 32768 places 158 against 175, 8192 51 against 53, 1024 14.3 against 13.9; bf16, 258 against
-  // 255, 73 against 73, 17.2 against 16.2. 64 sequences of 8 key heads of 128, E4M3: 715 against
-  // 779, 200 against 210, but 72 against 64 at 2048 (they spill, and items end more often).
+  // 32768 places 149 against 165, 8192 47 against 50, 1024 13.7 against 13.6; bf16, 247 against
+  // 254, 70 against 72, 18.5 against 18.0. 64 sequences of 8 key heads of 128, E4M3: 710 against
+  // 769, 199 against 206, but 68 against 63 at 2048 (they spill, and items end more often).
   static constexpr int kBlocks = FP8 && D == 64 ? 3 : 2;
   static constexpr int kStages = kBlocks == 3 ? 2 : 3;
   static constexpr int kSmem = kWarps * kStages * kStageBytes;

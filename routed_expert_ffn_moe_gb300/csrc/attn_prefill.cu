@@ -6,12 +6,13 @@
 // What bounds it: the tensor cores, 4 D flops per visible (query head, key) pair; next to them
 // the exponentials, one per pair, and the chain of latencies from S to P of a row tile.
 //
-// Measured, 64 query heads of 128 on 8 key heads: 2048 tokens over 20011 places in E4M3, 817 us, 1.73
-// PFLOP/s of 1.89 that a library's matrix product reaches; 8192 tokens, 650 us, 0.89 of it; 8 ragged
-// prompts of 65 to 3001 tokens, groups of 7, 321 us, 0.69 (one part in ten is the ends of units, when O
-// drains to memory, one in twelve the masked halves of diagonal tiles); 37 tokens, 8.5 us, latency.
-// Heads of 64 do half the work in a tile's time: 32 heads, 8192 tokens, 333 us, with a window of 1024,
-// 114 us, 0.30: per tile of 64 places 600 cycles of exponentials (both row tiles' warps together)
+// Measured in bursts of 20 ms, 64 query heads of 128 on 8 key heads: 2048 tokens over 20011 places in
+// E4M3, 784 us, 1.80 PFLOP/s of 1.89 that a library's matrix product reaches so; 8192 tokens, 656 us, 0.89
+// of it; 8 ragged prompts of 65 to 3001 tokens, groups of 7, 321 us, 0.69 (one part in ten is the ends
+// of units, when O drains to memory, one in twelve the masked halves of diagonal tiles); 37 tokens, 8.7
+// us, latency. Back to back for a second the card's power limit takes the clock from 2070 MHz to 1870
+// (1950 for the ragged prompts): 848 and 346 us. Heads of 64 do half the work in a tile's time: 32 heads,
+// 8192 tokens, 340 us, 0.43, with a window of 1024, 117 us, 0.29: per tile of 64 places 600 cycles of exponentials (both row tiles' warps together)
 // and 550 of loads, stores, votes and arrivals around them, against 512 of the tensor cores.
 //
 // Tiles. The G query heads of a key head share its keys, so a tile of 128 rows is 128/G
@@ -141,11 +142,11 @@ __device__ __forceinline__ uint64_t add_f32x2(uint64_t a, uint64_t b) {
 // unit, whose parts k_attn_prefill_join then joins; cuts that would leave less than kMinPart key tiles
 // on a side, or that fall into a unit of less than `min_split`, move to the unit's nearer end. A cut
 // costs about 10 us in all, a tile 0.7 us: where there are units enough for every run, units of less than 48
-// tiles stay whole, else of less than 16. Cut against whole, us: 1024 units of 18 tiles 129 against
-// 122; 8 prompts of 1024 tokens (512 units of up to 17) 158 against 141; 256 units of up to 345, 828
-// against 948. With few units: 16 tokens over 8192 places 32 against 79, over 2048 23 against 26;
-// of up to 9 tiles, 512 tokens, 28 against 21. A unit's start and end weighed as 4, 6, 8 tiles, us: 8
-// ragged prompts 320, 327, 343; one of 2048 tokens 66, 74, 72; one over 20011 places 806, 801, 820.
+// tiles stay whole, else of less than 16. Cut against whole, us: 1024 units of 18 tiles 126 against
+// 117; 8 prompts of 1024 tokens (512 units of up to 17) 149 against 135; 256 units of up to 345, 779
+// against 897. With few units: 16 tokens over 8192 places 32 against 71, over 2048 23 against 24;
+// of up to 9 tiles, 512 tokens, 26 against 19. A unit's start and end weighed as 4, 6, 8 tiles, us: 8
+// ragged prompts 321, 326, 342; one of 2048 tokens 66, 69, 71; one over 20011 places 779, 788, 780.
 constexpr int kUnitCost = 4 * kKeys, kMinPart = 4, kSplitFew = 16, kSplitMany = 48;
 
 // n / d of non-negative numbers: a 32-bit division where both fit
@@ -1048,7 +1049,8 @@ __global__ void __launch_bounds__(256) k_attn_prefill_join(const PrefillParams p
 // Copies what this step's tokens see into rows in order: E4M3 codes become bf16 exactly (the
 // scales stay outside), and places that no token sees but that share a tile with one are zeros.
 // Bound by HBM: one read of the visible cache and one bf16 write, against 2 G n flops an element for
-// n tokens a sequence. 22059 places of 8 key heads of 128, E4M3: 24 us, 0.83 of the copy rate.
+// n tokens a sequence. 22059 places of 8 key heads of 128, E4M3: 23 us, 0.87 of the copy rate. Its grid is
+// as wide as the tables: 64 sequences of 1 to 64 places, 55 us with tables of 64 places, 574 with tables of 131072.
 template <int D, bool FP8>
 __global__ void __launch_bounds__(256) k_attn_unpack(const AttnDims a, const uint8_t* k_cache,
                                                      const uint8_t* v_cache,
