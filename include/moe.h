@@ -146,6 +146,46 @@ MOE_API moe_status moe_route_hash(const moe_shape* shape, const void* x, const v
                                   const int32_t* tid2eid, int32_t vocab, int32_t* topk_idx,
                                   float* topk_w, void* ws, size_t ws_bytes, void* stream);
 
+/* Scored routing: softmax or sigmoid scores, a bias that balances the experts' load and only
+ * chooses, groups of experts of which some are kept, weights renormalised and scaled.
+ *   l  the token's E logits;  s = softmax(l) or 1 / (1 + exp(-l));  c = s + sel_bias (or s).
+ *   n_group > 1: the experts lie in n_group groups of E / n_group in a row; a group's value is the
+ *   sum of its group_top largest c; the topk_group groups of the largest values are kept.
+ *   topk_idx: the k largest c of the kept groups, by descending c, ties (of groups and of experts)
+ *   to the lower index.  topk_w = scale * s, or with renorm scale * s / (sum of the k s). */
+typedef enum {
+  MOE_SCORE_SOFTMAX = 0,
+  MOE_SCORE_SIGMOID = 1
+} moe_score;
+
+typedef struct {
+  int32_t score;       /* moe_score                                                           */
+  int32_t n_group;     /* groups of experts, 1 .. 32; E a multiple                            */
+  int32_t topk_group;  /* groups kept, 1 .. n_group; k <= topk_group * E / n_group            */
+  int32_t group_top;   /* experts whose c make a group's value: 1 or 2, <= E / n_group        */
+  int32_t renorm;      /* nonzero: the k weights are divided by their sum                     */
+  float scale;         /* of the weights; finite                                              */
+} moe_gate;
+
+/* The selection alone, from logits that the caller has.
+ *   logits   [T, E] fp32.   sel_bias [E] fp32, or NULL.
+ *   topk_idx [T, k] int32 out, topk_w [T, k] fp32 out (fp32 arithmetic).
+ * The choice is that of the formulas in 64-bit arithmetic: fp32 values nearer to each other than
+ * their error bounds are computed again in 64 bits. Without sel_bias the experts rank by their logits
+ * (the same order). A NaN c ranks below every number. Sigmoid weights of logits that are all
+ * -infinity are 0. Only T, E and k of `shape` are used (it must be valid); no workspace. */
+MOE_API moe_status moe_route_select(const moe_shape* shape, const moe_gate* gate,
+                                    const float* logits, const float* sel_bias,
+                                    int32_t* topk_idx, float* topk_w, void* stream);
+
+/* The router from the tokens: moe_route's logits (each in its fixed order, bias added to the logit),
+ * then the selection of moe_route_select. x, wg, bias, topk_idx, topk_w, ws as in moe_route (the
+ * status word is cleared: a layer starts here). */
+MOE_API moe_status moe_route_gate(const moe_shape* shape, const moe_gate* gate, const void* x,
+                                  const void* wg, const float* bias, const float* sel_bias,
+                                  int32_t* topk_idx, float* topk_w, void* ws, size_t ws_bytes,
+                                  void* stream);
+
 /* Token -> expert permutation ("第 6 章 超節點", 6.2.6).
  *   topk_idx       [T, k] int32, each row k distinct experts in [0, E).
  *   expert_offsets [E+2] int32 out: expert e (< E) owns slots [offsets[e], offsets[e+1]);
@@ -329,6 +369,78 @@ MOE_API moe_status moe_attn_prefill(const moe_attn_shape* shape, const void* q,
                                     const int32_t* block_table, const int32_t* kv_len,
                                     const int32_t* q_start, void* o, float* lse, void* ws,
                                     size_t ws_bytes, void* stream);
+
+/* ---- matrices in MXFP4 and their product ------------------------------------------------------
+ * The format of the MXFP4 expert weights: E2M1 codes, two a byte (element 2j of a row in the low
+ * nibble of byte j), one E8M0 scale 2^(e - 127) for every 32 consecutive elements of a row. Rows are
+ * packed: K / 2 bytes of codes each. The scales lie in one of two layouts:
+ *   rows   [rows, K/32] bytes, as the experts' s13 and s2;
+ *   tiles  as the tensor cores take them: for every 128 rows and every 128 elements of K a block of
+ *          512 bytes, blocks of the same rows in a row; the scale of row r, element 32 j lies in block
+ *          (r / 128, j / 4) at byte 16 (r % 32) + 4 (r % 128 / 32) + j % 4. Padding of K in the last
+ *          block of a row holds 127; padding rows hold anything. */
+typedef enum {
+  MOE_T_BF16 = 0,
+  MOE_T_F32 = 1,
+  MOE_T_MXFP4 = 2
+} moe_mx_dtype;
+
+typedef struct {
+  int32_t rows;      /* 0 .. 2^24                                                             */
+  int32_t K;         /* elements of a row: a multiple of 32, 32 .. 2^17                       */
+  int32_t dtype;     /* of the wide side: MOE_T_BF16 or MOE_T_F32                             */
+  int32_t tiles;     /* scales in tiles (nonzero) or in rows (0)                              */
+  int64_t stride;    /* elements between the rows of the wide side; 0: K. Multiple of 16 bytes */
+} moe_mx_rows;
+
+/* Bytes of the scale array of these rows; 0 for invalid ones. */
+MOE_API size_t moe_mx_scale_bytes(const moe_mx_rows* rows);
+
+/* x [rows, K] to MXFP4: for each 32 elements 2^(floor(log2 max|x|) - 2) as the scale (at least 2^-127;
+ * 1 if all are 0), elements divided by it and rounded to the nearest E2M1 value, ties to the even
+ * code, magnitudes above 6 to 6. A NaN or an infinity among the 32 makes the scale NaN (0xFF).
+ *   codes [rows, K/2] out, scales out (moe_mx_scale_bytes). */
+MOE_API moe_status moe_mx_quantize(const moe_mx_rows* rows, const void* x, void* codes,
+                                   void* scales, void* stream);
+
+/* The values back: y [rows, K] = code value * scale, exact in fp32 and, below 2^128, in bf16. A NaN
+ * scale gives NaNs. */
+MOE_API moe_status moe_mx_dequantize(const moe_mx_rows* rows, const void* codes,
+                                     const void* scales, void* y, void* stream);
+
+/* Scales in rows to scales in tiles (rows->rows and rows->K are used): once for a weight matrix that
+ * was stored with scales in rows. */
+MOE_API moe_status moe_mx_tile_scales(const moe_mx_rows* rows, const void* scales, void* tiles,
+                                      void* stream);
+
+typedef struct {
+  int32_t T;         /* rows of x and y, 0 .. 2^24                                            */
+  int32_t N;         /* rows of w: columns of y, 1 .. 2^20                                    */
+  int32_t K;         /* elements of a row of x and of w: a multiple of 32, 32 .. 2^17         */
+  int32_t x_dtype;   /* MOE_T_BF16: quantised by the call; MOE_T_MXFP4: codes and tiled scales */
+  int64_t x_stride;  /* elements between rows of a bf16 x; 0: K. A multiple of 8              */
+  int64_t y_stride;  /* elements between rows of y; 0: N                                      */
+  int64_t r_stride;  /* elements between rows of the residual; 0: N                           */
+} moe_mx_shape;
+
+/* Bytes of scratch for moe_mx_linear; 0 for an invalid shape. Its first 4 bytes are a device status
+ * word (moe_check_device_status reads it): zero before the first call. Nothing else needs
+ * initialisation, and one workspace may serve several shapes. */
+MOE_API size_t moe_mx_linear_workspace_size(const moe_mx_shape* shape);
+
+/* y = x w^T + bias + residual, both matrices in MXFP4, on block-scaled tensor-core products: the
+ * projections before and after the attention.
+ *   x        [T, K] bf16 (x_scales NULL; quantised as by moe_mx_quantize), or codes [T, K/2] with
+ *            x_scales in tiles.
+ *   w        codes [N, K/2], w_scales in tiles.
+ *   bias     [N] fp32, or NULL.   residual [T, N] bf16, or NULL; it may be y itself (same stride).
+ *   y        [T, N] bf16 out.
+ * Products are exact, sums are fp32, with one rounding to bf16 at the end. The result does not depend on the
+ * order in which blocks run. */
+MOE_API moe_status moe_mx_linear(const moe_mx_shape* shape, const void* x, const void* x_scales,
+                                 const void* w, const void* w_scales, const float* bias,
+                                 const void* residual, void* y, void* ws, size_t ws_bytes,
+                                 void* stream);
 
 /* Reads (and clears) the first device-side error recorded in `ws` since the last check.
  * Synchronises `stream`. Returns MOE_OK, MOE_ERR_DEVICE_BOUNDS or MOE_ERR_DEVICE_TIMEOUT (or

@@ -19,12 +19,20 @@ __all__ = ["MoeError", "MoeShape", "MOE_W_BF16", "MOE_W_FP8_E4M3_B128", "MOE_W_M
            "moe_last_error_string", "shape_of", "MoeLayer", "EXPORTED",
            "MoeAttnShape", "MOE_KV_BF16", "MOE_KV_FP8_E4M3", "attn_shape",
            "moe_attn_workspace_size", "moe_attn_workspace_zero_bytes", "moe_attn_append",
-           "moe_attn_decode", "moe_attn_prefill", "AttnLayer"]
+           "moe_attn_decode", "moe_attn_prefill", "AttnLayer",
+           "MoeGate", "MOE_SCORE_SOFTMAX", "MOE_SCORE_SIGMOID", "gate_of", "moe_route_select",
+           "moe_route_gate", "MoeMxRows", "MoeMxShape", "MOE_T_BF16", "MOE_T_F32", "MOE_T_MXFP4",
+           "mx_rows", "mx_shape", "moe_mx_scale_bytes", "moe_mx_quantize", "moe_mx_dequantize",
+           "moe_mx_tile_scales", "moe_mx_linear_workspace_size", "moe_mx_linear", "MxLinear"]
 
 MOE_W_BF16, MOE_W_FP8_E4M3_B128, MOE_W_MXFP4_E8M0_B32 = 0, 1, 2
 WDTYPES = {"bf16": MOE_W_BF16, "fp8": MOE_W_FP8_E4M3_B128, "mxfp4": MOE_W_MXFP4_E8M0_B32}
 MOE_KV_BF16, MOE_KV_FP8_E4M3 = 0, 1
 KV_DTYPES = {"bf16": MOE_KV_BF16, "fp8": MOE_KV_FP8_E4M3}
+MOE_SCORE_SOFTMAX, MOE_SCORE_SIGMOID = 0, 1
+SCORES = {"softmax": MOE_SCORE_SOFTMAX, "sigmoid": MOE_SCORE_SIGMOID}
+MOE_T_BF16, MOE_T_F32, MOE_T_MXFP4 = 0, 1, 2
+MX_DTYPES = {"bf16": MOE_T_BF16, "f32": MOE_T_F32, "mxfp4": MOE_T_MXFP4}
 STATUS = {0: "MOE_OK", -1: "MOE_ERR_INVALID_ARG", -2: "MOE_ERR_UNSUPPORTED",
           -3: "MOE_ERR_WORKSPACE", -4: "MOE_ERR_CUDA", -5: "MOE_ERR_DEVICE_TIMEOUT",
           -6: "MOE_ERR_DEVICE_BOUNDS"}
@@ -34,7 +42,10 @@ EXPORTED = ("moe_workspace_size", "moe_route", "moe_route_hash", "moe_route_noal
             "moe_check_device_status", "moe_selftest_bounded_wait", "moe_profile_enable",
             "moe_profile_read", "moe_last_error_string",
             "moe_attn_workspace_size", "moe_attn_workspace_zero_bytes", "moe_attn_append",
-            "moe_attn_decode", "moe_attn_prefill")
+            "moe_attn_decode", "moe_attn_prefill",
+            "moe_route_select", "moe_route_gate", "moe_mx_scale_bytes", "moe_mx_quantize",
+            "moe_mx_dequantize", "moe_mx_tile_scales", "moe_mx_linear_workspace_size",
+            "moe_mx_linear")
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 
@@ -63,6 +74,21 @@ class MoeAttnShape(ctypes.Structure):
                 + [(n, ctypes.c_int64) for n in
                    ("q_stride", "k_stride", "v_stride", "qr_stride", "o_stride", "page_stride",
                     "head_stride", "token_stride")])
+
+
+class MoeGate(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_int32) for n in ("score", "n_group", "topk_group", "group_top", "renorm")]
+                + [("scale", ctypes.c_float)])
+
+
+class MoeMxRows(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_int32) for n in ("rows", "K", "dtype", "tiles")]
+                + [("stride", ctypes.c_int64)])
+
+
+class MoeMxShape(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_int32) for n in ("T", "N", "K", "x_dtype")]
+                + [(n, ctypes.c_int64) for n in ("x_stride", "y_stride", "r_stride")])
 
 
 _lib = None
@@ -116,6 +142,24 @@ def load():
     L.moe_attn_decode.argtypes = [ashp] + [vp] * 10 + [sz, vp]
     L.moe_attn_prefill.restype = i32
     L.moe_attn_prefill.argtypes = [ashp] + [vp] * 11 + [sz, vp]
+    gate = ctypes.POINTER(MoeGate)
+    L.moe_route_select.restype = i32
+    L.moe_route_select.argtypes = [shp, gate] + [vp] * 5
+    L.moe_route_gate.restype = i32
+    L.moe_route_gate.argtypes = [shp, gate] + [vp] * 7 + [sz, vp]
+    rows, mshp = ctypes.POINTER(MoeMxRows), ctypes.POINTER(MoeMxShape)
+    L.moe_mx_scale_bytes.restype = sz
+    L.moe_mx_scale_bytes.argtypes = [rows]
+    L.moe_mx_quantize.restype = i32
+    L.moe_mx_quantize.argtypes = [rows] + [vp] * 4
+    L.moe_mx_dequantize.restype = i32
+    L.moe_mx_dequantize.argtypes = [rows] + [vp] * 4
+    L.moe_mx_tile_scales.restype = i32
+    L.moe_mx_tile_scales.argtypes = [rows] + [vp] * 3
+    L.moe_mx_linear_workspace_size.restype = sz
+    L.moe_mx_linear_workspace_size.argtypes = [mshp]
+    L.moe_mx_linear.restype = i32
+    L.moe_mx_linear.argtypes = [mshp] + [vp] * 8 + [sz, vp]
     L.moe_last_error_string.restype = ctypes.c_char_p
     L.moe_last_error_string.argtypes = []
     _lib = L
@@ -315,17 +359,93 @@ def moe_attn_prefill(shape, q, k_cache, v_cache, k_scale, v_scale, block_table, 
            "moe_attn_prefill")
 
 
+def gate_of(score="sigmoid", n_group=1, topk_group=1, group_top=2, renorm=True,
+            scale=1.0) -> MoeGate:
+    """moe_gate; score is "softmax", "sigmoid" or a MOE_SCORE_ number."""
+    return MoeGate(SCORES[score] if isinstance(score, str) else score, n_group, topk_group,
+                   group_top, int(renorm), scale)
+
+
+def moe_route_select(shape, gate, logits, sel_bias, topk_idx, topk_w, stream=None):
+    """The scored selection of each token's k experts from its logits [T, E] fp32."""
+    _check(load().moe_route_select(ctypes.byref(shape), ctypes.byref(gate), _ptr(logits),
+                                   _ptr(sel_bias), _ptr(topk_idx), _ptr(topk_w), _stream(stream)),
+           "moe_route_select")
+
+
+def moe_route_gate(shape, gate, x, wg, bias, sel_bias, topk_idx, topk_w, ws, stream=None,
+                   ws_bytes=None):
+    """The router with scored selection: moe_route's logits, then moe_route_select."""
+    wp, wb = _ws(ws)
+    _check(load().moe_route_gate(ctypes.byref(shape), ctypes.byref(gate), _ptr(x), _ptr(wg),
+                                 _ptr(bias), _ptr(sel_bias), _ptr(topk_idx), _ptr(topk_w), wp,
+                                 wb if ws_bytes is None else ws_bytes, _stream(stream)),
+           "moe_route_gate")
+
+
+def mx_rows(rows, K, dtype="bf16", tiles=False, stride=0) -> MoeMxRows:
+    """moe_mx_rows; a stride of 0 is K."""
+    return MoeMxRows(rows, K, MX_DTYPES[dtype] if isinstance(dtype, str) else dtype, int(tiles),
+                     stride)
+
+
+def mx_shape(T, N, K, x_dtype="bf16", x_stride=0, y_stride=0, r_stride=0) -> MoeMxShape:
+    """moe_mx_shape; a stride of 0 is the packed one."""
+    return MoeMxShape(T, N, K, MX_DTYPES[x_dtype] if isinstance(x_dtype, str) else x_dtype,
+                      x_stride, y_stride, r_stride)
+
+
+def moe_mx_scale_bytes(rows: MoeMxRows) -> int:
+    return int(load().moe_mx_scale_bytes(ctypes.byref(rows)))
+
+
+def moe_mx_quantize(rows, x, codes, scales, stream=None):
+    """x [rows, K] to MXFP4 codes [rows, K/2] and scales (moe_mx_scale_bytes)."""
+    _check(load().moe_mx_quantize(ctypes.byref(rows), _ptr(x), _ptr(codes), _ptr(scales),
+                                  _stream(stream)), "moe_mx_quantize")
+
+
+def moe_mx_dequantize(rows, codes, scales, y, stream=None):
+    """The values of MXFP4 rows into y [rows, K]."""
+    _check(load().moe_mx_dequantize(ctypes.byref(rows), _ptr(codes), _ptr(scales), _ptr(y),
+                                    _stream(stream)), "moe_mx_dequantize")
+
+
+def moe_mx_tile_scales(rows, scales, tiles, stream=None):
+    """Scales in rows to scales in tiles."""
+    _check(load().moe_mx_tile_scales(ctypes.byref(rows), _ptr(scales), _ptr(tiles),
+                                     _stream(stream)), "moe_mx_tile_scales")
+
+
+def moe_mx_linear_workspace_size(shape: MoeMxShape) -> int:
+    return int(load().moe_mx_linear_workspace_size(ctypes.byref(shape)))
+
+
+def moe_mx_linear(shape, x, x_scales, w, w_scales, bias, residual, y, ws, stream=None,
+                  ws_bytes=None):
+    """y = x w^T + bias + residual with both matrices in MXFP4."""
+    wp, wb = _ws(ws)
+    _check(load().moe_mx_linear(ctypes.byref(shape), _ptr(x), _ptr(x_scales), _ptr(w),
+                                _ptr(w_scales), _ptr(bias), _ptr(residual), _ptr(y), wp,
+                                wb if ws_bytes is None else ws_bytes, _stream(stream)),
+           "moe_mx_linear")
+
+
 class MoeLayer:
     """The four calls chained on one stream with buffers allocated once (torch, on `device`).
 
     weights: dict with wg [E,d] bf16, bias [E] f32 or None, w13, w2 (bf16, uint8 E4M3 codes or
     uint8 MXFP4 code pairs), s13, s2 (fp32 block scales, uint8 E8M0 scales, or None). `forward(x)` returns y [T,d] bf16; intermediate tensors
     stay available as attributes (topk_idx, topk_w, expert_offsets, perm_token, inv_slot, y_perm).
+
+    gate: a MoeGate (gate_of) for scored routing (moe_route_gate) instead of moe_route; the weights
+    may then hold sel_bias [E] f32.
     """
 
-    def __init__(self, T, d, E, k, f, n_shared, wdtype, weights, device="cuda"):
+    def __init__(self, T, d, E, k, f, n_shared, wdtype, weights, device="cuda", gate=None):
         import torch
         self.shape = shape_of(T, d, E, k, f, n_shared, wdtype)
+        self.gate = gate
         self.w = weights
         dev = torch.device(device)
         slots = T * k + n_shared * T
@@ -340,8 +460,11 @@ class MoeLayer:
         self.y = torch.empty(T, d, dtype=torch.bfloat16, device=dev)
 
     def forward(self, x, stream=None):
-        """The layer through moe_forward (one call; the shared expert overlaps the routing)."""
+        """The layer through moe_forward (one call; the shared expert overlaps the routing), or with a
+        gate as the four calls."""
         w = self.w
+        if self.gate is not None:
+            return self.forward_steps(x, stream)
         moe_forward(self.shape, x, w["wg"], w.get("bias"), w["w13"], w.get("s13"), w["w2"],
                     w.get("s2"), self.topk_idx, self.topk_w, self.expert_offsets, self.perm_token,
                     self.inv_slot, self.y_perm, self.y, self.ws, stream)
@@ -362,7 +485,11 @@ class MoeLayer:
     def forward_steps(self, x, stream=None):
         """The layer as the four separate calls."""
         w, s = self.w, self.shape
-        moe_route(s, x, w["wg"], w.get("bias"), self.topk_idx, self.topk_w, self.ws, stream)
+        if self.gate is not None:
+            moe_route_gate(s, self.gate, x, w["wg"], w.get("bias"), w.get("sel_bias"),
+                           self.topk_idx, self.topk_w, self.ws, stream)
+        else:
+            moe_route(s, x, w["wg"], w.get("bias"), self.topk_idx, self.topk_w, self.ws, stream)
         moe_permute(s, self.topk_idx, self.expert_offsets, self.perm_token, self.inv_slot, self.ws,
                     stream)
         moe_expert_ffn(s, x, self.perm_token, self.expert_offsets, w["w13"], w.get("s13"),
@@ -485,4 +612,86 @@ class AttnLayer:
 
     def check(self, stream=None):
         """Raises MoeError if a step since the last check met something out of range."""
+        moe_check_device_status(self.ws, stream)
+
+
+class MxLinear:
+    """A projection with MXFP4 weights, y = x W^T + bias + residual, its scales laid out in tiles and its
+    workspace and output allocated once (torch, on `device`).
+
+    codes [N, K/2] and scales [N, K/32] uint8 as the MXFP4 expert weights have them (or
+    `MxLinear.from_weight`); bias [N] fp32 or None. `forward(x, residual)` takes x [T, K] bf16, whose
+    rows may lie apart, and residual [T, N] bf16 or None, at most max_tokens rows, and returns
+    y [T, N] bf16: `out`, or the layer's own buffer, which the next forward overwrites. Tensors of
+    another type, size, layout or device raise ValueError.
+    """
+
+    def __init__(self, codes, scales, bias=None, max_tokens=4096, device="cuda"):
+        import torch
+        dev = torch.device(device)
+        if dev.type == "cuda" and dev.index is None:
+            dev = torch.device("cuda", torch.cuda.current_device())
+        self._bf16, self._dev = torch.bfloat16, dev
+        N, K = codes.shape[0], 2 * codes.shape[1]
+        for name, t, dt, shape in (("codes", codes, torch.uint8, (N, K // 2)),
+                                   ("scales", scales, torch.uint8, (N, K // 32)),
+                                   ("bias", bias, torch.float32, (N,))):
+            if t is not None and (t.dtype != dt or tuple(t.shape) != shape or t.device != dev
+                                  or not t.is_contiguous()):
+                raise ValueError(f"{name}: {t.dtype}, {tuple(t.shape)}, strides {t.stride()} on "
+                                 f"{t.device}: packed {dt} {shape} on {dev} is needed")
+        self._own(N, K, codes, bias, max_tokens)
+        moe_mx_tile_scales(mx_rows(N, K, tiles=True), scales, self.w_scales)
+
+    def _own(self, N, K, codes, bias, max_tokens):
+        import torch
+        n = moe_mx_linear_workspace_size(mx_shape(max_tokens, N, K))
+        if n == 0:
+            raise MoeError(-1, "MxLinear", moe_last_error_string())
+        self.N, self.K, self.max_tokens = N, K, max_tokens
+        self.codes, self.bias = codes, bias
+        self.w_scales = torch.empty(moe_mx_scale_bytes(mx_rows(N, K, tiles=True)),
+                                    dtype=torch.uint8, device=self._dev)
+        self.ws = torch.empty(n, dtype=torch.uint8, device=self._dev)
+        self.ws[:4].zero_()
+        self.y = torch.empty(max_tokens, N, dtype=torch.bfloat16, device=self._dev)
+
+    @classmethod
+    def from_weight(cls, weight, bias=None, max_tokens=4096):
+        """The projection of a weight [N, K] in bf16 or fp32 (rows packed), quantised here."""
+        import torch
+        kind = {torch.bfloat16: "bf16", torch.float32: "f32"}.get(weight.dtype)
+        if kind is None or weight.dim() != 2 or not weight.is_contiguous():
+            raise ValueError(f"weight: {weight.dtype}, {tuple(weight.shape)}, strides "
+                             f"{weight.stride()}: packed [N, K] in bf16 or fp32 is needed")
+        N, K = weight.shape
+        codes = torch.empty(N, K // 2, dtype=torch.uint8, device=weight.device)
+        scales = torch.empty(N, K // 32, dtype=torch.uint8, device=weight.device)
+        moe_mx_quantize(mx_rows(N, K, kind), weight, codes, scales)
+        return cls(codes, scales, bias, max_tokens, weight.device)
+
+    def _rows_apart(self, name, t, T, n):
+        """The distance of the T rows of n packed bf16."""
+        if (t.dtype == self._bf16 and t.device == self._dev and t.dim() == 2
+                and tuple(t.shape) == (T, n)):
+            if t.is_contiguous():
+                return n
+            if t[0].is_contiguous() and t.stride(0) >= n:
+                return t.stride(0)
+        raise ValueError(f"{name}: {t.dtype}, {tuple(t.shape)}, strides {t.stride()} on {t.device}: "
+                         f"{T} rows of {n} packed bf16 on {self._dev} are needed")
+
+    def forward(self, x, residual=None, out=None, stream=None):
+        T = x.shape[0]
+        if T > self.max_tokens:
+            raise ValueError(f"{T} tokens: the layer was made for {self.max_tokens}")
+        y = self.y[:T] if out is None else out
+        s = mx_shape(T, self.N, self.K, "bf16", self._rows_apart("x", x, T, self.K),
+                     self._rows_apart("out", y, T, self.N),
+                     0 if residual is None else self._rows_apart("residual", residual, T, self.N))
+        moe_mx_linear(s, x, None, self.codes, self.w_scales, self.bias, residual, y, self.ws, stream)
+        return y
+
+    def check(self, stream=None):
+        """Raises MoeError if a call since the last check gave up a wait."""
         moe_check_device_status(self.ws, stream)

@@ -27,7 +27,6 @@ moe_status cuda_fail(cudaError_t e, const char* where) {
   return fail(MOE_ERR_CUDA, "%s: %s", where, cudaGetErrorString(e));
 }
 
-namespace {
 moe_status check_shape(const moe_shape* s) {
   if (!s) return fail(MOE_ERR_INVALID_ARG, "shape is NULL");
   if (s->E < 1 || s->E > 1024) return fail(MOE_ERR_INVALID_ARG, "E=%d not in [1, 1024]", s->E);
@@ -47,6 +46,8 @@ moe_status check_shape(const moe_shape* s) {
   return MOE_OK;
 }
 
+namespace {
+
 // Expert weights and their scales: bf16 has none; E4M3 and MXFP4 need both. MXFP4 code arrays
 // are read through tensor maps that want 32-byte aligned bases.
 moe_status check_weights(const moe_shape* s, const void* w13, const void* s13, const void* w2,
@@ -63,6 +64,8 @@ moe_status check_weights(const moe_shape* s, const void* w13, const void* s13, c
   return MOE_OK;
 }
 
+}  // namespace
+
 moe_status check_ws(const moe_shape* s, const void* ws, size_t ws_bytes, WsLayout* L) {
   REQUIRE_PTR(ws, 256);
   *L = ws_layout(*s);
@@ -70,8 +73,6 @@ moe_status check_ws(const moe_shape* s, const void* ws, size_t ws_bytes, WsLayou
     return fail(MOE_ERR_WORKSPACE, "workspace %zu bytes < %zu required", ws_bytes, L->total);
   return MOE_OK;
 }
-
-}  // namespace
 
 // ---- profiling session ------------------------------------------------------------------
 namespace {

@@ -9,6 +9,9 @@ namespace moe {
 moe_status fail(moe_status st, const char* fmt, ...) __attribute__((format(printf, 2, 3)));
 moe_status cuda_fail(cudaError_t e, const char* where);
 
+moe_status check_shape(const moe_shape* s);
+moe_status check_ws(const moe_shape* s, const void* ws, size_t ws_bytes, WsLayout* L);
+
 inline bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
 }  // namespace moe

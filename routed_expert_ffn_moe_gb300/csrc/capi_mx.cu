@@ -1,0 +1,152 @@
+// The C ABI of the MXFP4 operators (include/moe.h): host-side validation and dispatch.
+#include "capi.h"
+#include "mx.h"
+
+namespace moe {
+namespace {
+
+moe_status check_k(int K) {
+  if (K < 32 || K > (1 << 17) || K % 32)
+    return fail(MOE_ERR_INVALID_ARG, "K=%d not a multiple of 32 in [32, 2^17]", K);
+  return MOE_OK;
+}
+
+// `given` elements between rows of at least `row`, or the packed rows if 0; offsets fit 63 bits
+moe_status take(const char* name, int64_t given, int64_t row, int multiple, int64_t* out) {
+  *out = given ? given : row;
+  if (*out < row || *out > (int64_t)1 << 36 || *out % multiple)
+    return fail(MOE_ERR_INVALID_ARG, "%s=%lld not a multiple of %d of at least %lld elements", name,
+                (long long)given, multiple, (long long)row);
+  return MOE_OK;
+}
+
+moe_status check_rows(const moe_mx_rows* s, MxRows* r) {
+  if (!s) return fail(MOE_ERR_INVALID_ARG, "rows is NULL");
+  if (s->rows < 0 || s->rows > (1 << 24))
+    return fail(MOE_ERR_INVALID_ARG, "rows=%d not in [0, 2^24]", s->rows);
+  if (s->dtype != MOE_T_BF16 && s->dtype != MOE_T_F32)
+    return fail(MOE_ERR_INVALID_ARG, "dtype=%d: bf16 or fp32 is needed", s->dtype);
+  moe_status st = check_k(s->K);
+  if (st != MOE_OK) return st;
+  r->rows = s->rows;
+  r->K = s->K;
+  r->f32 = s->dtype == MOE_T_F32;
+  r->tiles = s->tiles != 0;
+  return take("stride", s->stride, s->K, r->f32 ? 4 : 8, &r->stride);
+}
+
+moe_status check_linear(const moe_mx_shape* s, MxDims* d) {
+  if (!s) return fail(MOE_ERR_INVALID_ARG, "shape is NULL");
+  if (s->T < 0 || s->T > (1 << 24))
+    return fail(MOE_ERR_INVALID_ARG, "T=%d not in [0, 2^24]", s->T);
+  if (s->N < 1 || s->N > (1 << 20))
+    return fail(MOE_ERR_INVALID_ARG, "N=%d not in [1, 2^20]", s->N);
+  moe_status st = check_k(s->K);
+  if (st != MOE_OK) return st;
+  if (s->x_dtype != MOE_T_BF16 && s->x_dtype != MOE_T_MXFP4)
+    return fail(MOE_ERR_INVALID_ARG, "x_dtype=%d: bf16 or MXFP4 is needed", s->x_dtype);
+  d->T = s->T;
+  d->N = s->N;
+  d->K = s->K;
+  d->quantised = s->x_dtype == MOE_T_MXFP4;
+  if (d->quantised && s->x_stride)
+    return fail(MOE_ERR_INVALID_ARG, "x_stride=%lld: rows of codes are packed",
+                (long long)s->x_stride);
+  if ((st = take("x_stride", s->x_stride, s->K, 8, &d->x_stride)) != MOE_OK) return st;
+  if ((st = take("y_stride", s->y_stride, s->N, 1, &d->y_stride)) != MOE_OK) return st;
+  return take("r_stride", s->r_stride, s->N, 1, &d->r_stride);
+}
+
+}  // namespace
+}  // namespace moe
+
+using namespace moe;
+
+extern "C" {
+
+size_t moe_mx_scale_bytes(const moe_mx_rows* rows) {
+  MxRows r;
+  return check_rows(rows, &r) == MOE_OK ? mx_scale_bytes(r) : 0;
+}
+
+moe_status moe_mx_quantize(const moe_mx_rows* rows, const void* x, void* codes, void* scales,
+                           void* stream) {
+  MxRows r;
+  moe_status st = check_rows(rows, &r);
+  if (st != MOE_OK) return st;
+  if (r.rows == 0) return MOE_OK;
+  REQUIRE_PTR(x, 16);
+  REQUIRE_PTR(codes, 16);
+  REQUIRE_PTR(scales, 16);
+  cudaError_t e = launch_mx_quantize(r, x, static_cast<uint8_t*>(codes),
+                                     static_cast<uint8_t*>(scales),
+                                     static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? MOE_OK : cuda_fail(e, "moe_mx_quantize launch");
+}
+
+moe_status moe_mx_dequantize(const moe_mx_rows* rows, const void* codes, const void* scales,
+                             void* y, void* stream) {
+  MxRows r;
+  moe_status st = check_rows(rows, &r);
+  if (st != MOE_OK) return st;
+  if (r.rows == 0) return MOE_OK;
+  REQUIRE_PTR(codes, 16);
+  REQUIRE_PTR(scales, 16);
+  REQUIRE_PTR(y, 16);
+  cudaError_t e = launch_mx_dequantize(r, static_cast<const uint8_t*>(codes),
+                                       static_cast<const uint8_t*>(scales), y,
+                                       static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? MOE_OK : cuda_fail(e, "moe_mx_dequantize launch");
+}
+
+moe_status moe_mx_tile_scales(const moe_mx_rows* rows, const void* scales, void* tiles,
+                              void* stream) {
+  MxRows r;
+  moe_status st = check_rows(rows, &r);
+  if (st != MOE_OK) return st;
+  if (r.rows == 0) return MOE_OK;
+  REQUIRE_PTR(scales, 16);
+  REQUIRE_PTR(tiles, 16);
+  if (scales == tiles) return fail(MOE_ERR_INVALID_ARG, "scales and tiles are the same array");
+  cudaError_t e = launch_mx_tile_scales(r.rows, r.K, static_cast<const uint8_t*>(scales),
+                                        static_cast<uint8_t*>(tiles),
+                                        static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? MOE_OK : cuda_fail(e, "moe_mx_tile_scales launch");
+}
+
+size_t moe_mx_linear_workspace_size(const moe_mx_shape* shape) {
+  MxDims d;
+  return check_linear(shape, &d) == MOE_OK ? mx_ws(d).total : 0;
+}
+
+moe_status moe_mx_linear(const moe_mx_shape* shape, const void* x, const void* x_scales,
+                         const void* w, const void* w_scales, const float* bias,
+                         const void* residual, void* y, void* ws, size_t ws_bytes, void* stream) {
+  MxDims d;
+  moe_status st = check_linear(shape, &d);
+  if (st != MOE_OK) return st;
+  REQUIRE_PTR(ws, 256);
+  const MxWs L = mx_ws(d);
+  if (ws_bytes < L.total)
+    return fail(MOE_ERR_WORKSPACE, "workspace %zu bytes < %zu required", ws_bytes, L.total);
+  if (d.T == 0) return MOE_OK;
+  REQUIRE_PTR(x, 16);
+  if (d.quantised) REQUIRE_PTR(x_scales, 16);
+  if (!d.quantised && x_scales)
+    return fail(MOE_ERR_INVALID_ARG, "x_scales must be NULL for a bf16 x");
+  REQUIRE_PTR(w, 16);
+  REQUIRE_PTR(w_scales, 16);
+  REQUIRE_PTR(y, 16);
+  if (!aligned(bias, 16)) return fail(MOE_ERR_INVALID_ARG, "bias not 16-byte aligned");
+  if (!aligned(residual, 16)) return fail(MOE_ERR_INVALID_ARG, "residual not 16-byte aligned");
+  if (residual == y && d.r_stride != d.y_stride)
+    return fail(MOE_ERR_INVALID_ARG, "residual is y but r_stride=%lld is not y_stride=%lld",
+                (long long)d.r_stride, (long long)d.y_stride);
+  cudaError_t e = launch_mx_linear(
+      d, x, static_cast<const uint8_t*>(x_scales), static_cast<const uint8_t*>(w),
+      static_cast<const uint8_t*>(w_scales), bias, static_cast<const uint16_t*>(residual),
+      static_cast<uint16_t*>(y), static_cast<char*>(ws), L, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? MOE_OK : cuda_fail(e, "moe_mx_linear launch");
+}
+
+}  // extern "C"

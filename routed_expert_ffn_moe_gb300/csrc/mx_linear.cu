@@ -1,0 +1,333 @@
+// y = x w^T + bias + residual, both matrices in MXFP4, on block-scaled tcgen05.mma (kind::mxf4: 64 of
+// K an instruction, one E8M0 scale per row and 32 of K, fp32 sums in TMEM).
+//
+// The weights are the M side (128 rows a tile), the tokens the N side, so that a single token streams
+// each weight byte once at full tile width. A stage holds 256 of K: one 128-byte swizzle row of
+// codes a matrix row and two 512-byte blocks of scales a side, which tcgen05.cp carries to TMEM ahead of the
+// stage's four MMAs. Few tiles are split along K over the CTAs of a cluster; their fp32 sums meet in
+// distributed shared memory, added in the order of K.
+#include "mx_quant.cuh"
+#include "tc_common.cuh"
+
+namespace moe {
+namespace {
+
+using namespace ptx;
+using namespace tc;
+
+constexpr int kStageK = 256;
+constexpr uint32_t kRowBytes = kStageK / 2;
+constexpr uint32_t kSfBytes = 2 * kMxTile;  // a stage's scales of 128 rows
+constexpr int kLinThreads = 192;  // warps: 0 loads, 1 MMAs, 2..5 quantise x, then read the sums
+
+struct LinParams {
+  int T, N, K;
+  int mtiles;   // tiles of 128 rows of w
+  int splits;   // CTAs of a cluster, along K
+  int chunks;   // 128-wide blocks of K
+  int64_t x_stride, y_stride, r_stride;
+  const uint16_t* x;        // bf16, quantised by the warps
+  const uint8_t* x_scales;  // or tiles of scales
+  const uint8_t* w_scales;
+  const float* bias;
+  const uint16_t* residual;
+  uint16_t* y;
+  int vec;  // rows of y and of the residual: 8-byte accesses
+  int* status;
+};
+
+template <int NT, int STAGES>
+struct LinSmem {
+  static constexpr uint32_t kA = kBM * kRowBytes;
+  static constexpr uint32_t kB = NT * kRowBytes;
+  static constexpr uint32_t kTiles = STAGES * (kA + kB);
+  static constexpr uint32_t kScales = STAGES * 2 * kSfBytes;
+  static constexpr uint32_t kPart = NT * kBM * 4;  // the sums, over the tiles once they are read
+  static constexpr uint32_t kBars = 8 * (2 * STAGES + 1) + 16;
+  static constexpr uint32_t kTotal = kTiles + kScales + kBars + 1024;
+  static constexpr uint32_t kSfCol = NT;  // scales: 2 x (8 columns of A, 8 of B)
+  static constexpr uint32_t kCols = NT + 32 <= 64 ? 64 : NT + 32 <= 128 ? 128 : 256;
+};
+
+// One value of y: the sum, the bias and the residual, rounded once.
+__device__ __forceinline__ float with_residual(float v, uint16_t r) {
+  return v + __uint_as_float((uint32_t)r << 16);
+}
+
+template <int NT, int STAGES, bool QUANT>
+__global__ void __launch_bounds__(kLinThreads)
+    k_mx_linear(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_x,
+                const LinParams p) {
+  using S = LinSmem<NT, STAGES>;
+  static_assert(S::kPart <= S::kTiles, "the sums fit over the tiles");
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~uintptr_t(1023));
+  uint8_t* sm_b = smem + STAGES * S::kA;
+  uint8_t* sm_sf = smem + S::kTiles;  // per stage: of w, of x
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + S::kTiles + S::kScales);
+  uint64_t* empty = full + STAGES;
+  uint64_t* acc_full = empty + STAGES;
+  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(acc_full + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < STAGES; ++s) {
+      mbar_init(&full[s], QUANT ? 5 : 1);  // the loads, and the four quantising warps
+      mbar_init(&empty[s], 1);
+    }
+    mbar_init(acc_full, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+    prefetch_tmap(&tm_w);
+    if (!QUANT) prefetch_tmap(&tm_x);
+  }
+  if (warp == 1) {
+    tmem_alloc(tmem_holder, S::kCols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_holder;
+
+  const int rank = (int)(blockIdx.x % (unsigned)p.splits);
+  const int tile = (int)(blockIdx.x / (unsigned)p.splits);
+  const int mt = tile % p.mtiles, tt = tile / p.mtiles;
+  const int row0 = mt * kBM, tok0 = tt * NT;
+  const int ntok = min(NT, p.T - tok0);
+  const int npad = (ntok + 15) & ~15;
+  const int nst = (p.chunks + 1) >> 1;
+  const int k0 = (int)((long)nst * rank / p.splits), k1 = (int)((long)nst * (rank + 1) / p.splits);
+
+  pdl_wait_then_release();
+
+  if (warp == 0) {
+    if (lane == 0) {
+      uint32_t stage = 0, phase = 0;
+      const uint64_t pol_w = policy_evict_first(), pol_x = policy_evict_last();
+      for (int kb = k0; kb < k1; ++kb) {
+        if (!wait_bar(&empty[stage], phase ^ 1u, abort_flag, p.status)) break;
+        const uint32_t sf = (uint32_t)min(2, p.chunks - 2 * kb) * kMxTile;
+        mbar_arrive_expect_tx(&full[stage], S::kA + sf + (QUANT ? 0u : S::kB + sf));
+        tma_load_2d(smem + stage * S::kA, &tm_w, &full[stage], kb * (int)kRowBytes, row0, pol_w);
+        bulk_load(sm_sf + stage * 2 * kSfBytes,
+                  p.w_scales + ((size_t)mt * p.chunks + 2 * kb) * kMxTile, sf, &full[stage]);
+        if (!QUANT) {
+          tma_load_2d(sm_b + stage * S::kB, &tm_x, &full[stage], kb * (int)kRowBytes, tok0, pol_x);
+          bulk_load(sm_sf + (stage * 2 + 1) * kSfBytes,
+                    p.x_scales + ((size_t)(tok0 >> 7) * p.chunks + 2 * kb) * kMxTile, sf,
+                    &full[stage]);
+        }
+        if (++stage == STAGES) { stage = 0; phase ^= 1u; }
+      }
+      // the loads in flight land before the block leaves
+      for (int s = 0; s < STAGES; ++s) {
+        const uint32_t issued = s < (int)stage ? phase : phase ^ 1u;
+        drain_bar(&full[s], issued, p.status);
+      }
+    }
+  } else if (warp == 1) {
+    if (lane == 0) {
+      uint32_t stage = 0, phase = 0;
+      bool ok = true;
+      for (int kb = k0; kb < k1; ++kb) {
+        if (!wait_bar(&full[stage], phase, abort_flag, p.status)) { ok = false; break; }
+        tc_fence_after();
+        const int n64 = min(4, (p.K - kb * kStageK + 63) >> 6);  // of K there is
+        const uint32_t sf = tmem + S::kSfCol + (uint32_t)(kb & 1) * 16;
+        const uint32_t sa = smem_u32(sm_sf + stage * 2 * kSfBytes), sb = sa + kSfBytes;
+        for (int c = 0; 2 * c < n64; ++c) {
+          tmem_cp_scales(sf + 4 * c, scale_desc(sa + c * kMxTile));
+          tmem_cp_scales(sf + 8 + 4 * c, scale_desc(sb + c * kMxTile));
+        }
+        const uint64_t ad = sw128_desc(smem_u32(smem + stage * S::kA));
+        const uint64_t bd = sw128_desc(smem_u32(sm_b + stage * S::kB));
+        for (int j = 0; j < n64; ++j)
+          mma_mxf4(tmem, ad + 2 * j, bd + 2 * j, idesc_mxf4(kBM, npad, 2 * (j & 1)),
+                   sf + 4 * (j >> 1), sf + 8 + 4 * (j >> 1), (kb > k0 || j) ? 1u : 0u);
+        mma_commit(&empty[stage]);
+        if (++stage == STAGES) { stage = 0; phase ^= 1u; }
+      }
+      if (ok) mma_commit(acc_full);
+    }
+  } else {
+    const int w = warp - 2;
+    if (QUANT) {
+      // warp w quantises rows w, w + 4, ... of the stage into the swizzled tile and its scales
+      uint32_t stage = 0, phase = 0;
+      for (int kb = k0; kb < k1; ++kb) {
+        const int k = kb * kStageK + 8 * lane;
+        if (!__all_sync(0xffffffffu, wait_bar(&empty[stage], phase ^ 1u, abort_flag, p.status))) break;
+        uint8_t* b = sm_b + stage * S::kB;
+        uint8_t* sf = sm_sf + (stage * 2 + 1) * kSfBytes;
+        for (int n = w; n < ntok; n += 4) {
+          uint4 u = make_uint4(0, 0, 0, 0);
+          if (k < p.K) u = ldg_u4(p.x + (int64_t)(tok0 + n) * p.x_stride + k);
+          float v[8];
+          mxq::bf16x8(u, v);
+          const uint32_t s = mxq::quad_scale(v);
+          const float f = mxq::inverse(s);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) v[i] = s == 255u ? 0.f : v[i] * f;
+          *reinterpret_cast<uint32_t*>(b + n * kRowBytes + (((lane >> 2) ^ (n & 7)) << 4) +
+                                       (lane & 3) * 4) = mxq::codes8(v);
+          if ((lane & 3) == 0) {
+            const int j = lane >> 2;
+            sf[(j >> 2) * kMxTile + (n & 31) * 16 + (n >> 5) * 4 + (j & 3)] = (uint8_t)s;
+          }
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&full[stage]);
+        if (++stage == STAGES) { stage = 0; phase ^= 1u; }
+      }
+      __syncwarp();
+    }
+    // the sums: lane = row of w, column = token
+    if (__all_sync(0xffffffffu, wait_bar(acc_full, 0, abort_flag, p.status))) {
+      tc_fence_after();
+      const int qd = warp & 3;
+      float* part = reinterpret_cast<float*>(smem) + qd * 32 + lane;
+      for (int c0 = 0; c0 < npad; c0 += 16) {
+        uint32_t r[16];
+        tmem_ld16(tmem + ((uint32_t)(qd * 32) << 16) + c0, r);
+        tmem_ld_wait(r);
+#pragma unroll
+        for (int j = 0; j < 16; ++j) part[(c0 + j) * kBM] = __uint_as_float(r[j]);
+      }
+      tc_fence_before();
+    }
+  }
+  __syncwarp();
+  if (p.splits > 1) cluster_sync();
+  else __syncthreads();
+
+  // rank r of the cluster finishes its share of the tile's sums, four rows of w at a time
+  {
+    const int total = ntok * (kBM / 4);
+    const int q1 = (int)((long)total * (rank + 1) / p.splits);
+    const uint32_t base = smem_u32(smem);
+    for (int q = (int)((long)total * rank / p.splits) + threadIdx.x; q < q1; q += kLinThreads) {
+      const int n = q >> 5, feat = row0 + 4 * (q & 31);
+      if (feat >= p.N) continue;
+      float v[4] = {0.f, 0.f, 0.f, 0.f};
+      for (int s = 0; s < p.splits; ++s) {
+        const float4 a = p.splits > 1 ? ld_cluster_f4(mapa_shared(base + 16 * q, s))
+                                      : *reinterpret_cast<const float4*>(smem + 16 * q);
+        v[0] += a.x;
+        v[1] += a.y;
+        v[2] += a.z;
+        v[3] += a.w;
+      }
+      uint16_t* y = p.y + (int64_t)(tok0 + n) * p.y_stride + feat;
+      const uint16_t* res = p.residual + (int64_t)(tok0 + n) * p.r_stride + feat;
+      if (p.bias) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] += feat + i < p.N ? __ldg(p.bias + feat + i) : 0.f;
+      }
+      if (p.vec && feat + 3 < p.N) {
+        if (p.residual) {
+          const uint2 r = *reinterpret_cast<const uint2*>(res);
+          v[0] = with_residual(v[0], (uint16_t)r.x);
+          v[1] = with_residual(v[1], (uint16_t)(r.x >> 16));
+          v[2] = with_residual(v[2], (uint16_t)r.y);
+          v[3] = with_residual(v[3], (uint16_t)(r.y >> 16));
+        }
+        uint2 o;
+        o.x = f32_to_bf16_rn(v[0]) | (uint32_t)f32_to_bf16_rn(v[1]) << 16;
+        o.y = f32_to_bf16_rn(v[2]) | (uint32_t)f32_to_bf16_rn(v[3]) << 16;
+        *reinterpret_cast<uint2*>(y) = o;
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (feat + i < p.N)
+            y[i] = f32_to_bf16_rn(p.residual ? with_residual(v[i], res[i]) : v[i]);
+      }
+    }
+  }
+  __syncwarp();
+  if (p.splits > 1) cluster_sync();  // no block leaves while another reads its sums
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, S::kCols);
+  }
+}
+
+template <int NT, int STAGES, bool QUANT>
+cudaError_t launch_tile(const CUtensorMap& w, const CUtensorMap& x, const LinParams& p, int tiles,
+                        cudaStream_t st) {
+  using S = LinSmem<NT, STAGES>;
+  static_assert(S::kTotal <= 227 * 1024, "shared memory");
+  auto kern = k_mx_linear<NT, STAGES, QUANT>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       (int)S::kTotal);
+  if (e != cudaSuccess) return e;
+  count_launches(1);
+  const dim3 grid((unsigned)tiles * (unsigned)p.splits), block(kLinThreads);
+  return p.splits > 1
+             ? launch_pdl_cluster(kern, grid, block, S::kTotal, st, (unsigned)p.splits, w, x, p)
+             : launch_pdl(kern, grid, block, S::kTotal, st, w, x, p);
+}
+
+// Tokens up to which the product's own warps quantise x, so that a call is one launch.
+constexpr int kQuantTokens = 32;
+
+}  // namespace
+
+cudaError_t launch_mx_linear(const MxDims& d, const void* x, const uint8_t* x_scales,
+                             const uint8_t* w, const uint8_t* w_scales, const float* bias,
+                             const uint16_t* residual, uint16_t* y, char* ws, const MxWs& L,
+                             cudaStream_t st) {
+  if (d.T == 0) return cudaSuccess;
+  cudaError_t e = cudaSuccess;
+  const bool fused = !d.quantised && d.T <= kQuantTokens;
+  const uint8_t* codes = static_cast<const uint8_t*>(x);
+  if (!d.quantised && !fused) {
+    const MxRows r{d.T, d.K, false, true, d.x_stride};
+    uint8_t* c = reinterpret_cast<uint8_t*>(ws + L.codes);
+    uint8_t* s = reinterpret_cast<uint8_t*>(ws + L.scales);
+    if ((e = launch_mx_quantize(r, x, c, s, st)) != cudaSuccess) return e;
+    codes = c;
+    x_scales = s;
+  }
+  LinParams p{};
+  p.T = d.T;
+  p.N = d.N;
+  p.K = d.K;
+  p.mtiles = (d.N + kBM - 1) / kBM;
+  p.chunks = mx_chunks(d.K);
+  p.x_stride = d.x_stride;
+  p.y_stride = d.y_stride;
+  p.r_stride = d.r_stride;
+  p.x = fused ? static_cast<const uint16_t*>(x) : nullptr;
+  p.x_scales = x_scales;
+  p.w_scales = w_scales;
+  p.bias = bias;
+  p.residual = residual;
+  p.y = y;
+  p.vec = d.y_stride % 4 == 0 && (!residual || d.r_stride % 4 == 0);
+  p.status = reinterpret_cast<int*>(ws + L.status);
+  const int nt = d.T <= 16 ? 16 : d.T <= 32 ? 32 : d.T <= 64 ? 64 : 128;
+  const int tiles = p.mtiles * ((d.T + nt - 1) / nt);
+  const int nst = (p.chunks + 1) / 2;
+  p.splits = 1;
+  while (p.splits < 8 && 2 * p.splits <= nst && tiles * 2 * p.splits <= 2 * num_sms()) p.splits *= 2;
+  CUtensorMap mw, mx;
+  if ((e = encode_u8_2d(&mw, w, d.N, d.K / 2, kBM)) != cudaSuccess) return e;
+  mx = mw;
+  if (!fused && (e = encode_u8_2d(&mx, codes, d.T, d.K / 2, nt)) != cudaSuccess) return e;
+  if (nt == 16)
+    return fused ? launch_tile<16, 5, true>(mw, mx, p, tiles, st)
+                 : launch_tile<16, 5, false>(mw, mx, p, tiles, st);
+  if (nt == 32)
+    return fused ? launch_tile<32, 5, true>(mw, mx, p, tiles, st)
+                 : launch_tile<32, 5, false>(mw, mx, p, tiles, st);
+  if (nt == 64) return launch_tile<64, 4, false>(mw, mx, p, tiles, st);
+  return launch_tile<128, 6, false>(mw, mx, p, tiles, st);
+}
+
+}  // namespace moe
