@@ -6,35 +6,15 @@
 // codes a matrix row and two 512-byte blocks of scales a side, which tcgen05.cp carries to TMEM ahead of the
 // stage's four MMAs. Few tiles are split along K over the CTAs of a cluster; their fp32 sums meet in
 // distributed shared memory, added in the order of K.
+#include "mx_linear.cuh"
 #include "mx_quant.cuh"
-#include "tc_common.cuh"
 
 namespace moe {
 namespace {
 
-using namespace ptx;
-using namespace tc;
+using namespace mxl;
 
-constexpr int kStageK = 256;
-constexpr uint32_t kRowBytes = kStageK / 2;
-constexpr uint32_t kSfBytes = 2 * kMxTile;  // a stage's scales of 128 rows
 constexpr int kLinThreads = 192;  // warps: 0 loads, 1 MMAs, 2..5 quantise x, then read the sums
-
-struct LinParams {
-  int T, N, K;
-  int mtiles;   // tiles of 128 rows of w
-  int splits;   // CTAs of a cluster, along K
-  int chunks;   // 128-wide blocks of K
-  int64_t x_stride, y_stride, r_stride;
-  const uint16_t* x;        // bf16, quantised by the warps
-  const uint8_t* x_scales;  // or tiles of scales
-  const uint8_t* w_scales;
-  const float* bias;
-  const uint16_t* residual;
-  uint16_t* y;
-  int vec;  // rows of y and of the residual: 8-byte accesses
-  int* status;
-};
 
 template <int NT, int STAGES>
 struct LinSmem {
@@ -49,13 +29,8 @@ struct LinSmem {
   static constexpr uint32_t kCols = NT + 32 <= 64 ? 64 : NT + 32 <= 128 ? 128 : 256;
 };
 
-// One value of y: the sum, the bias and the residual, rounded once.
-__device__ __forceinline__ float with_residual(float v, uint16_t r) {
-  return v + __uint_as_float((uint32_t)r << 16);
-}
-
 template <int NT, int STAGES, bool QUANT>
-__global__ void __launch_bounds__(kLinThreads)
+__global__ void __launch_bounds__(kLinThreads, 2)
     k_mx_linear(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_x,
                 const LinParams p) {
   using S = LinSmem<NT, STAGES>;
@@ -104,7 +79,7 @@ __global__ void __launch_bounds__(kLinThreads)
   pdl_wait_then_release();
 
   if (warp == 0) {
-    if (lane == 0) {
+    if (elect_one()) {
       uint32_t stage = 0, phase = 0;
       const uint64_t pol_w = policy_evict_first(), pol_x = policy_evict_last();
       for (int kb = k0; kb < k1; ++kb) {
@@ -129,7 +104,7 @@ __global__ void __launch_bounds__(kLinThreads)
       }
     }
   } else if (warp == 1) {
-    if (lane == 0) {
+    if (elect_one()) {
       uint32_t stage = 0, phase = 0;
       bool ok = true;
       for (int kb = k0; kb < k1; ++kb) {
@@ -311,6 +286,10 @@ cudaError_t launch_mx_linear(const MxDims& d, const void* x, const uint8_t* x_sc
   p.y = y;
   p.vec = d.y_stride % 4 == 0 && (!residual || d.r_stride % 4 == 0);
   p.status = reinterpret_cast<int*>(ws + L.status);
+  if (d.T > 128) {
+    p.vec = d.y_stride % 8 == 0 && (!residual || d.r_stride % 8 == 0);
+    return launch_pair(p, codes, w, st);
+  }
   const int nt = d.T <= 16 ? 16 : d.T <= 32 ? 32 : d.T <= 64 ? 64 : 128;
   const int tiles = p.mtiles * ((d.T + nt - 1) / nt);
   const int nst = (p.chunks + 1) / 2;

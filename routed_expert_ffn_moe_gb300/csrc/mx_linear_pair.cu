@@ -1,0 +1,297 @@
+// The MXFP4 product for many tokens: a persistent GEMM on CTA pairs (tcgen05.mma.cta_group::2).
+//
+// A tile is 256 tokens x BN features, K in stages of 256. The tokens are the M side, so that a thread of
+// the epilogue holds a run of consecutive features of one token and stores it 16 bytes at a time. Each
+// CTA of the pair loads its own 128 tokens and half of the tile's weight rows; the scales of all BN
+// weight rows go to both.
+//
+//   warp 0     TMA: codes and scales of both sides, all completing on the even CTA's stage barrier
+//   warp 1     (even CTA) scales to TMEM (tcgen05.cp), four MMAs of 64 of K a stage
+//   warps 2-9  epilogue: a lane quadrant and half of the features each. The sums leave TMEM for registers at
+//              once (packed to bf16, bias and residual added), and TMEM is handed back before the
+//              first store: with one accumulator of 256 columns beside the scales' the next tile's MMAs wait
+//              for that alone.
+#include "mx_linear.cuh"
+
+namespace moe {
+namespace mxl {
+namespace {
+
+constexpr int kPairThreads = 320;
+
+template <int BN, int STAGES>
+struct PairSmem {
+  static constexpr uint32_t kA = kBM * kRowBytes;          // this CTA's tokens
+  static constexpr uint32_t kB = BN / 2 * kRowBytes;       // its half of the weight rows
+  static constexpr uint32_t kTileBytes = kA + kB;
+  static constexpr int kBlocks = BN / 128;                 // 128-row blocks of weight scales
+  static constexpr uint32_t kSf = (1 + kBlocks) * kSfBytes;
+  static constexpr uint32_t kStageBytes = kTileBytes + kSf;
+  static constexpr uint32_t kBars = 8 * (2 * STAGES + 2) + 16;
+  static constexpr uint32_t kTotal = STAGES * kStageBytes + kBars + 1024;
+  static constexpr uint32_t kSfCols = 8 + 8 * kBlocks;     // of a stage: tokens, then weights
+};
+
+template <int BN, int STAGES, bool RES>
+__global__ void __launch_bounds__(kPairThreads, 1)
+    k_mx_linear_pair(const __grid_constant__ CUtensorMap tm_x,
+                     const __grid_constant__ CUtensorMap tm_w,
+                     const __grid_constant__ CUtensorMap tm_xs,
+                     const __grid_constant__ CUtensorMap tm_ws, const LinParams p, int ttiles,
+                     int ftiles) {
+  using S = PairSmem<BN, STAGES>;
+  static_assert(BN == 128 || BN == 256, "MMA N");
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~uintptr_t(1023));
+  uint8_t* sm_sf = smem + STAGES * S::kTileBytes;
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + STAGES * S::kStageBytes);
+  uint64_t* empty = full + STAGES;
+  uint64_t* acc_full = empty + STAGES;
+  uint64_t* acc_empty = acc_full + 1;
+  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(acc_empty + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = (int)cluster_ctarank();
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < STAGES; ++s) {
+      mbar_init(&full[s], 1);   // the even CTA's loading thread, and both CTAs' bytes
+      mbar_init(&empty[s], 1);  // the commit of the stage's MMAs
+    }
+    mbar_init(acc_full, 1);
+    mbar_init(acc_empty, 16);  // the epilogue warps of both CTAs
+    *abort_flag = 0;
+    fence_mbar_init();
+    prefetch_tmap(&tm_x);
+    prefetch_tmap(&tm_w);
+    prefetch_tmap(&tm_xs);
+    prefetch_tmap(&tm_ws);
+  }
+  if (warp == 1) {
+    tmem_alloc_pair(tmem_holder, 512);
+    tmem_relinquish_pair();
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();  // both CTAs' barriers are initialised before either signals the other
+  tc_fence_after();
+  const uint32_t tmem = *tmem_holder;
+  const int tile0 = (int)(blockIdx.x >> 1), tstep = (int)(gridDim.x >> 1);
+  const int total = ttiles * ftiles;
+  const int nst = (p.chunks + 1) >> 1;
+
+  pdl_wait_then_release();
+
+  if (warp == 0) {
+    if (elect_one()) {
+      const uint64_t pol = policy_evict_normal();
+      const uint32_t full0 = mapa_shared(smem_u32(&full[0]), 0);
+      uint32_t stage = 0, phase = 0;
+      bool ok = true;
+      for (int tile = tile0; ok && tile < total; tile += tstep) {
+        const int tt = tile / ftiles, ft = tile - tt * ftiles;
+        const int tok = tt * 256 + rank * 128, feat = ft * BN + rank * (BN / 2);
+        const int xs = (tt * 2 + rank) * p.chunks, ws = ft * S::kBlocks * p.chunks;
+        for (int kb = 0; kb < nst; ++kb) {
+          if (!wait_bar(&empty[stage], phase ^ 1u, abort_flag, p.status)) { ok = false; break; }
+          if (rank == 0) mbar_arrive_expect_tx(&full[stage], 2 * S::kStageBytes);
+          const uint32_t bar = full0 + 8u * stage;
+          uint8_t* a = smem + stage * S::kTileBytes;
+          uint8_t* sf = sm_sf + stage * S::kSf;
+          tma_load_2d_pair(a, &tm_x, bar, kb * (int)kRowBytes, tok, pol);
+          tma_load_2d_pair(a + S::kA, &tm_w, bar, kb * (int)kRowBytes, feat, pol);
+          // boxes of two 512-byte blocks; beyond K or the last row they hold anything, or zeros
+          tma_load_2d_pair(sf, &tm_xs, bar, 0, xs + 2 * kb, pol);
+#pragma unroll
+          for (int b = 0; b < S::kBlocks; ++b)
+            tma_load_2d_pair(sf + (1 + b) * kSfBytes, &tm_ws, bar, 0, ws + b * p.chunks + 2 * kb,
+                             pol);
+          if (++stage == STAGES) { stage = 0; phase ^= 1u; }
+        }
+      }
+      // the loads in flight land, and the commits for both CTAs' stages arrive, before a CTA leaves
+      for (int s = 0; s < STAGES; ++s) {
+        const uint32_t issued = s < (int)stage ? phase : phase ^ 1u;
+        if (rank == 0) drain_bar(&full[s], issued, p.status);
+        drain_bar(&empty[s], issued, p.status);
+      }
+    }
+  } else if (warp == 1) {
+    // one elected thread: under a comparison of lane numbers a stage's MMAs took 1.5 times as long
+    if (rank == 0 && elect_one()) {
+      uint32_t stage = 0, phase = 0, it = 0, acc_phase = 0;
+      bool ok = true;
+      for (int tile = tile0; ok && tile < total; tile += tstep) {
+        if (!wait_bar(acc_empty, acc_phase ^ 1u, abort_flag, p.status)) break;
+        tc_fence_after();
+        for (int kb = 0; kb < nst; ++kb, ++it) {
+          if (!wait_bar(&full[stage], phase, abort_flag, p.status)) { ok = false; break; }
+          tc_fence_after();
+          const int n64 = min(4, (p.K - kb * kStageK + 63) >> 6);
+          const uint32_t sfa = tmem + BN + (it & 1) * S::kSfCols, sfb = sfa + 8;
+          const uint32_t sm = smem_u32(sm_sf + stage * S::kSf);
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            if (2 * c >= n64) break;
+            tmem_cp_scales_pair(sfa + 4 * c, scale_desc(sm + c * kMxTile));
+#pragma unroll
+            for (int b = 0; b < S::kBlocks; ++b)
+              tmem_cp_scales_pair(sfb + c * 4 * S::kBlocks + 4 * b,
+                                  scale_desc(sm + (1 + b) * kSfBytes + c * kMxTile));
+          }
+          const uint32_t st = smem_u32(smem + stage * S::kTileBytes);
+          const uint64_t ad = sw128_desc(st), bd = sw128_desc(st + S::kA);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            if (j >= n64) break;
+            mma_mxf4_pair(tmem, ad + 2 * j, bd + 2 * j, idesc_mxf4(256, BN, 2 * (j & 1)),
+                          sfa + 4 * (j >> 1), sfb + (j >> 1) * 4 * S::kBlocks,
+                          (kb | j) ? 1u : 0u);
+          }
+          mma_commit_pair(&empty[stage]);
+          if (++stage == STAGES) { stage = 0; phase ^= 1u; }
+        }
+        if (!ok) break;
+        mma_commit_pair(acc_full);
+        acc_phase ^= 1u;
+      }
+    }
+  } else {
+    const int qd = warp & 3, half = (warp - 2) >> 2;
+    constexpr int kCols = BN / 2;  // features of a thread
+    const uint32_t empty0 = mapa_shared(smem_u32(acc_empty), 0);
+    uint32_t acc_phase = 0;
+    for (int tile = tile0; tile < total; tile += tstep) {
+      const int tt = tile / ftiles, ft = tile - tt * ftiles;
+      const int tok = tt * 256 + rank * 128 + qd * 32 + lane;
+      const int feat = ft * BN + half * kCols;
+      const bool row = tok < p.T;
+      const bool whole = p.vec && feat + kCols <= p.N;
+      uint32_t out[kCols / 2];  // the residual, then the results in its place
+      const uint16_t* rp = p.residual + (int64_t)tok * p.r_stride + feat;
+      if (RES) {
+        if (whole && row) {
+#pragma unroll
+          for (int i = 0; i < kCols / 8; ++i) {
+            const uint4 u = reinterpret_cast<const uint4*>(rp)[i];
+            out[4 * i] = u.x;
+            out[4 * i + 1] = u.y;
+            out[4 * i + 2] = u.z;
+            out[4 * i + 3] = u.w;
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < kCols; i += 2)
+            out[i / 2] = row ? (feat + i < p.N ? rp[i] : 0u) |
+                                   (feat + i + 1 < p.N ? (uint32_t)rp[i + 1] << 16 : 0u)
+                             : 0u;
+        }
+      }
+      if (!__all_sync(0xffffffffu, wait_bar(acc_full, acc_phase, abort_flag, p.status))) break;
+      acc_phase ^= 1u;
+      tc_fence_after();
+#pragma unroll
+      for (int c = 0; c < kCols; c += 32) {
+        uint32_t r[32];
+        tmem_ld32(tmem + ((uint32_t)(qd * 32) << 16) + half * kCols + c, r);
+        tmem_ld_wait32(r);
+#pragma unroll
+        for (int i = 0; i < 32; i += 2) {
+          float v0 = __uint_as_float(r[i]), v1 = __uint_as_float(r[i + 1]);
+          if (p.bias) {
+            const int f = feat + c + i;
+            v0 += f < p.N ? __ldg(p.bias + f) : 0.f;
+            v1 += f + 1 < p.N ? __ldg(p.bias + f + 1) : 0.f;
+          }
+          if (RES) {
+            v0 = with_residual(v0, (uint16_t)out[(c + i) / 2]);
+            v1 = with_residual(v1, (uint16_t)(out[(c + i) / 2] >> 16));
+          }
+          out[(c + i) / 2] = f32_to_bf16_rn(v0) | (uint32_t)f32_to_bf16_rn(v1) << 16;
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_cluster(empty0);
+      if (row) {
+        uint16_t* y = p.y + (int64_t)tok * p.y_stride + feat;
+        if (whole) {
+#pragma unroll
+          for (int i = 0; i < kCols / 8; ++i)
+            reinterpret_cast<uint4*>(y)[i] =
+                make_uint4(out[4 * i], out[4 * i + 1], out[4 * i + 2], out[4 * i + 3]);
+        } else {
+#pragma unroll
+          for (int i = 0; i < kCols; ++i)
+            if (feat + i < p.N) y[i] = (uint16_t)(out[i / 2] >> (16 * (i & 1)));
+        }
+      }
+    }
+  }
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();  // no CTA leaves while its peer may still signal it
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc_pair(tmem, 512);
+  }
+}
+
+// Scales in tiles as rows of 512 bytes, boxes of two rows, as they lie.
+cudaError_t encode_scales(CUtensorMap* m, const uint8_t* base, uint64_t blocks) {
+  EncodeTiledFn fn = encode_fn();
+  if (!fn) return cudaErrorNotSupported;
+  const cuuint64_t dims[2] = {kMxTile / 4, blocks};
+  const cuuint64_t strides[1] = {kMxTile};
+  const cuuint32_t box[2] = {kMxTile / 4, 2};
+  const cuuint32_t estr[2] = {1, 1};
+  const CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT32, 2, const_cast<uint8_t*>(base), dims,
+                        strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                        CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
+template <int BN, int STAGES, bool RES>
+cudaError_t launch_bn(const LinParams& p, const uint8_t* codes, const uint8_t* w,
+                      cudaStream_t st) {
+  using S = PairSmem<BN, STAGES>;
+  static_assert(S::kTotal <= 227 * 1024, "shared memory");
+  static_assert(BN + 2 * S::kSfCols <= 512, "TMEM columns");
+  CUtensorMap mx, mw, mxs, mws;
+  cudaError_t e = encode_u8_2d(&mx, codes, p.T, p.K / 2, 128);
+  if (e == cudaSuccess) e = encode_u8_2d(&mw, w, p.N, p.K / 2, BN / 2);
+  if (e == cudaSuccess) e = encode_scales(&mxs, p.x_scales, (uint64_t)((p.T + 127) / 128) * p.chunks);
+  if (e == cudaSuccess) e = encode_scales(&mws, p.w_scales, (uint64_t)((p.N + 127) / 128) * p.chunks);
+  if (e != cudaSuccess) return e;
+  auto kern = k_mx_linear_pair<BN, STAGES, RES>;
+  e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)S::kTotal);
+  if (e != cudaSuccess) return e;
+  const int ttiles = (p.T + 255) / 256, ftiles = (p.N + BN - 1) / BN;
+  const long total = (long)ttiles * ftiles;
+  const long pairs = num_sms() / 2;
+  count_launches(1);
+  return launch_pdl_cluster(kern, dim3((unsigned)(2 * (total < pairs ? total : pairs))),
+                            dim3(kPairThreads), S::kTotal, st, 2u, mx, mw, mxs, mws, p, ttiles,
+                            ftiles);
+}
+
+}  // namespace
+
+cudaError_t launch_pair(const LinParams& p, const uint8_t* codes, const uint8_t* w,
+                        cudaStream_t st) {
+  // 256 features a tile, or 128 where that makes the longest pair's share of tiles shorter
+  const long pairs = num_sms() / 2, tt = (p.T + 255) / 256;
+  const long n256 = (tt * ((p.N + 255) / 256) + pairs - 1) / pairs * 2;
+  const long n128 = (tt * ((p.N + 127) / 128) + pairs - 1) / pairs;
+  if (n128 < n256)
+    return p.residual ? launch_bn<128, 7, true>(p, codes, w, st)
+                      : launch_bn<128, 7, false>(p, codes, w, st);
+  return p.residual ? launch_bn<256, 6, true>(p, codes, w, st)
+                    : launch_bn<256, 6, false>(p, codes, w, st);
+}
+
+}  // namespace mxl
+}  // namespace moe

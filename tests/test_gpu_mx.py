@@ -220,7 +220,7 @@ def product(T, N, K, kind="bf16", bias=False, residual=False, seed=0, xs=0, ys=0
 
 
 @pytest.mark.parametrize("kind", ["bf16", "mxfp4"])
-@pytest.mark.parametrize("T", [1, 2, 15, 16, 17, 32, 33, 64, 65, 127, 128, 129, 300])
+@pytest.mark.parametrize("T", [1, 2, 15, 16, 17, 32, 33, 64, 65, 127, 128, 129, 255, 256, 257, 300, 513])
 def test_tokens(T, kind):
     product(T, 256, 512, kind)
 
@@ -228,19 +228,19 @@ def test_tokens(T, kind):
 @pytest.mark.parametrize("kind", ["bf16", "mxfp4"])
 @pytest.mark.parametrize("N", [1, 2, 7, 127, 128, 129, 131, 1000])
 def test_features(N, kind):
-    for T in (3, 70, 140):
+    for T in (3, 70, 140, 400):
         product(T, N, 256, kind, bias=True, residual=True)
 
 
 @pytest.mark.parametrize("kind", ["bf16", "mxfp4"])
 @pytest.mark.parametrize("K", [32, 64, 96, 128, 160, 192, 256, 288, 320, 480, 2048, 2080, 7168, 16384])
 def test_widths(K, kind):
-    for T in (5, 40, 200):
+    for T in (5, 40, 200, 520):
         product(T, 200, K, kind, seed=K)
 
 
 def test_strides():
-    for T in (4, 24, 150):
+    for T in (4, 24, 150, 300):
         product(T, 130, 256, xs=264, ys=137, rs=135, bias=True, residual=True)
         product(T, 128, 256, xs=512, ys=256, rs=140, residual=True)
         product(T, 130, 256, ys=130, residual=True, alias=True)
