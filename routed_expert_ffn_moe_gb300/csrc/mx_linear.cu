@@ -83,7 +83,7 @@ __global__ void __launch_bounds__(kLinThreads, 2)
       uint32_t stage = 0, phase = 0;
       const uint64_t pol_w = policy_evict_first(), pol_x = policy_evict_last();
       for (int kb = k0; kb < k1; ++kb) {
-        if (!wait_bar(&empty[stage], phase ^ 1u, abort_flag, p.status)) break;
+        if (!wait_phase(&empty[stage], phase ^ 1u, abort_flag, p.status)) break;
         const uint32_t sf = (uint32_t)min(2, p.chunks - 2 * kb) * kMxTile;
         mbar_arrive_expect_tx(&full[stage], S::kA + sf + (QUANT ? 0u : S::kB + sf));
         tma_load_2d(smem + stage * S::kA, &tm_w, &full[stage], kb * (int)kRowBytes, row0, pol_w);
@@ -108,7 +108,7 @@ __global__ void __launch_bounds__(kLinThreads, 2)
       uint32_t stage = 0, phase = 0;
       bool ok = true;
       for (int kb = k0; kb < k1; ++kb) {
-        if (!wait_bar(&full[stage], phase, abort_flag, p.status)) { ok = false; break; }
+        if (!wait_phase(&full[stage], phase, abort_flag, p.status)) { ok = false; break; }
         tc_fence_after();
         const int n64 = min(4, (p.K - kb * kStageK + 63) >> 6);  // of K there is
         const uint32_t sf = tmem + S::kSfCol + (uint32_t)(kb & 1) * 16;
@@ -134,7 +134,7 @@ __global__ void __launch_bounds__(kLinThreads, 2)
       uint32_t stage = 0, phase = 0;
       for (int kb = k0; kb < k1; ++kb) {
         const int k = kb * kStageK + 8 * lane;
-        if (!__all_sync(0xffffffffu, wait_bar(&empty[stage], phase ^ 1u, abort_flag, p.status))) break;
+        if (!__all_sync(0xffffffffu, wait_phase(&empty[stage], phase ^ 1u, abort_flag, p.status))) break;
         uint8_t* b = sm_b + stage * S::kB;
         uint8_t* sf = sm_sf + (stage * 2 + 1) * kSfBytes;
         for (int n = w; n < ntok; n += 4) {
@@ -161,7 +161,7 @@ __global__ void __launch_bounds__(kLinThreads, 2)
       __syncwarp();
     }
     // the sums: lane = row of w, column = token
-    if (__all_sync(0xffffffffu, wait_bar(acc_full, 0, abort_flag, p.status))) {
+    if (__all_sync(0xffffffffu, wait_phase(acc_full, 0, abort_flag, p.status))) {
       tc_fence_after();
       const int qd = warp & 3;
       float* part = reinterpret_cast<float*>(smem) + qd * 32 + lane;

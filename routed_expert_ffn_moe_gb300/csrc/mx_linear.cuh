@@ -30,6 +30,25 @@ struct LinParams {
   int* status;
 };
 
+// Bounded wait on an mbarrier phase, as wait_bar, but the clock is first read after 64 tries.
+__device__ __forceinline__ bool wait_phase(uint64_t* bar, uint32_t parity, volatile int* abort_flag,
+                                           int* status) {
+  uint64_t t0 = 0;
+  for (uint32_t i = 1;; ++i) {
+    if (mbar_try_wait(bar, parity)) return true;
+    if ((i & 63u) == 0) {
+      if (*abort_flag) return false;
+      const uint64_t t = globaltimer();
+      if (t0 == 0) t0 = t;
+      if (t - t0 > kWaitLimitNs) {
+        record_error(status, MOE_ERR_DEVICE_TIMEOUT);
+        *abort_flag = 1;
+        return false;
+      }
+    }
+  }
+}
+
 // One value of y: the sum, the bias and the residual, rounded once.
 __device__ __forceinline__ float with_residual(float v, uint16_t r) {
   return v + __uint_as_float((uint32_t)r << 16);

@@ -18,6 +18,7 @@ namespace mxl {
 namespace {
 
 constexpr int kPairThreads = 320;
+constexpr uint32_t kOutBytes = 32 * 128;  // 32 tokens x 64 features of bf16, one swizzle row a token
 
 template <int BN, int STAGES>
 struct PairSmem {
@@ -27,8 +28,9 @@ struct PairSmem {
   static constexpr int kBlocks = BN / 128;                 // 128-row blocks of weight scales
   static constexpr uint32_t kSf = (1 + kBlocks) * kSfBytes;
   static constexpr uint32_t kStageBytes = kTileBytes + kSf;
-  static constexpr uint32_t kBars = 8 * (2 * STAGES + 2) + 16;
-  static constexpr uint32_t kTotal = STAGES * kStageBytes + kBars + 1024;
+  static constexpr uint32_t kOut = 8 * kOutBytes;          // a box of the output for each epilogue warp
+  static constexpr uint32_t kBars = 8 * (2 * STAGES + 2 + 8) + 16;
+  static constexpr uint32_t kTotal = STAGES * kStageBytes + kOut + kBars + 1024;
   static constexpr uint32_t kSfCols = 8 + 8 * kBlocks;     // of a stage: tokens, then weights
 };
 
@@ -37,19 +39,23 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     k_mx_linear_pair(const __grid_constant__ CUtensorMap tm_x,
                      const __grid_constant__ CUtensorMap tm_w,
                      const __grid_constant__ CUtensorMap tm_xs,
-                     const __grid_constant__ CUtensorMap tm_ws, const LinParams p, int ttiles,
+                     const __grid_constant__ CUtensorMap tm_ws,
+                     const __grid_constant__ CUtensorMap tm_y,
+                     const __grid_constant__ CUtensorMap tm_r, const LinParams p, int ttiles,
                      int ftiles) {
   using S = PairSmem<BN, STAGES>;
   static_assert(BN == 128 || BN == 256, "MMA N");
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~uintptr_t(1023));
-  uint8_t* sm_sf = smem + STAGES * S::kTileBytes;
-  uint64_t* full = reinterpret_cast<uint64_t*>(smem + STAGES * S::kStageBytes);
+  uint8_t* sm_out = smem + STAGES * S::kTileBytes;
+  uint8_t* sm_sf = sm_out + S::kOut;
+  uint64_t* full = reinterpret_cast<uint64_t*>(sm_sf + STAGES * S::kSf);
   uint64_t* empty = full + STAGES;
   uint64_t* acc_full = empty + STAGES;
   uint64_t* acc_empty = acc_full + 1;
-  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(acc_empty + 1);
+  uint64_t* res_full = acc_empty + 1;  // of each epilogue warp: its residual has landed
+  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(res_full + 8);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -61,6 +67,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     }
     mbar_init(acc_full, 1);
     mbar_init(acc_empty, 16);  // the epilogue warps of both CTAs
+    for (int w = 0; w < 8; ++w) mbar_init(&res_full[w], 1);
     *abort_flag = 0;
     fence_mbar_init();
     prefetch_tmap(&tm_x);
@@ -94,7 +101,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
         const int tok = tt * 256 + rank * 128, feat = ft * BN + rank * (BN / 2);
         const int xs = (tt * 2 + rank) * p.chunks, ws = ft * S::kBlocks * p.chunks;
         for (int kb = 0; kb < nst; ++kb) {
-          if (!wait_bar(&empty[stage], phase ^ 1u, abort_flag, p.status)) { ok = false; break; }
+          if (!wait_phase(&empty[stage], phase ^ 1u, abort_flag, p.status)) { ok = false; break; }
           if (rank == 0) mbar_arrive_expect_tx(&full[stage], 2 * S::kStageBytes);
           const uint32_t bar = full0 + 8u * stage;
           uint8_t* a = smem + stage * S::kTileBytes;
@@ -123,10 +130,10 @@ __global__ void __launch_bounds__(kPairThreads, 1)
       uint32_t stage = 0, phase = 0, it = 0, acc_phase = 0;
       bool ok = true;
       for (int tile = tile0; ok && tile < total; tile += tstep) {
-        if (!wait_bar(acc_empty, acc_phase ^ 1u, abort_flag, p.status)) break;
+        if (!wait_phase(acc_empty, acc_phase ^ 1u, abort_flag, p.status)) break;
         tc_fence_after();
         for (int kb = 0; kb < nst; ++kb, ++it) {
-          if (!wait_bar(&full[stage], phase, abort_flag, p.status)) { ok = false; break; }
+          if (!wait_phase(&full[stage], phase, abort_flag, p.status)) { ok = false; break; }
           tc_fence_after();
           const int n64 = min(4, (p.K - kb * kStageK + 63) >> 6);
           const uint32_t sfa = tmem + BN + (it & 1) * S::kSfCols, sfb = sfa + 8;
@@ -161,73 +168,102 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     const int qd = warp & 3, half = (warp - 2) >> 2;
     constexpr int kCols = BN / 2;  // features of a thread
     const uint32_t empty0 = mapa_shared(smem_u32(acc_empty), 0);
-    uint32_t acc_phase = 0;
+    uint8_t* box = sm_out + (warp - 2) * kOutBytes;
+    uint8_t* my = box + lane * 128;
+    uint64_t* rbar = &res_full[warp - 2];
+    uint32_t acc_phase = 0, res_phase = 0;
     for (int tile = tile0; tile < total; tile += tstep) {
       const int tt = tile / ftiles, ft = tile - tt * ftiles;
-      const int tok = tt * 256 + rank * 128 + qd * 32 + lane;
+      const int tok0 = tt * 256 + rank * 128 + qd * 32;
       const int feat = ft * BN + half * kCols;
-      const bool row = tok < p.T;
-      const bool whole = p.vec && feat + kCols <= p.N;
-      uint32_t out[kCols / 2];  // the residual, then the results in its place
-      const uint16_t* rp = p.residual + (int64_t)tok * p.r_stride + feat;
-      if (RES) {
-        if (whole && row) {
-#pragma unroll
-          for (int i = 0; i < kCols / 8; ++i) {
-            const uint4 u = reinterpret_cast<const uint4*>(rp)[i];
-            out[4 * i] = u.x;
-            out[4 * i + 1] = u.y;
-            out[4 * i + 2] = u.z;
-            out[4 * i + 3] = u.w;
+      // the residual of 64 features into the box, once the store before it has been read
+      const auto fetch = [&](int f0) {
+        if (!RES || tok0 >= p.T || f0 >= p.N) return;
+        if (p.vec) {
+          if (lane == 0) {
+            bulk_wait_read();
+            mbar_arrive_expect_tx(rbar, kOutBytes);
+            tma_load_2d(box, &tm_r, rbar, f0, tok0, policy_evict_first());
           }
         } else {
-#pragma unroll
-          for (int i = 0; i < kCols; i += 2)
-            out[i / 2] = row ? (feat + i < p.N ? rp[i] : 0u) |
-                                   (feat + i + 1 < p.N ? (uint32_t)rp[i + 1] << 16 : 0u)
-                             : 0u;
+          __syncwarp();
+          for (int r = 0; r < 32 && tok0 + r < p.T; ++r)
+            for (int e = lane; e < 64 && f0 + e < p.N; e += 32)
+              *reinterpret_cast<uint16_t*>(box + r * 128 + (((e >> 3) ^ (r & 7)) << 4) +
+                                           (e & 7) * 2) =
+                  p.residual[(int64_t)(tok0 + r) * p.r_stride + f0 + e];
+          __syncwarp();
         }
+      };
+      fetch(feat);
+      const bool ok =
+          __all_sync(0xffffffffu, wait_phase(acc_full, acc_phase, abort_flag, p.status));
+      if (!ok) {
+        if (RES && p.vec && tok0 < p.T && feat < p.N) drain_bar(rbar, res_phase, p.status);
+        break;
       }
-      if (!__all_sync(0xffffffffu, wait_bar(acc_full, acc_phase, abort_flag, p.status))) break;
       acc_phase ^= 1u;
       tc_fence_after();
+      uint32_t r[kCols];
 #pragma unroll
-      for (int c = 0; c < kCols; c += 32) {
-        uint32_t r[32];
-        tmem_ld32(tmem + ((uint32_t)(qd * 32) << 16) + half * kCols + c, r);
-        tmem_ld_wait32(r);
+      for (int c = 0; c < kCols; c += 32)
+        tmem_ld32(tmem + ((uint32_t)(qd * 32) << 16) + half * kCols + c, r + c);
 #pragma unroll
-        for (int i = 0; i < 32; i += 2) {
-          float v0 = __uint_as_float(r[i]), v1 = __uint_as_float(r[i + 1]);
-          if (p.bias) {
-            const int f = feat + c + i;
-            v0 += f < p.N ? __ldg(p.bias + f) : 0.f;
-            v1 += f + 1 < p.N ? __ldg(p.bias + f + 1) : 0.f;
-          }
-          if (RES) {
-            v0 = with_residual(v0, (uint16_t)out[(c + i) / 2]);
-            v1 = with_residual(v1, (uint16_t)(out[(c + i) / 2] >> 16));
-          }
-          out[(c + i) / 2] = f32_to_bf16_rn(v0) | (uint32_t)f32_to_bf16_rn(v1) << 16;
-        }
-      }
+      for (int c = 0; c < kCols; c += 32) tmem_ld_wait32(r + c);
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive_cluster(empty0);
-      if (row) {
-        uint16_t* y = p.y + (int64_t)tok * p.y_stride + feat;
-        if (whole) {
 #pragma unroll
-          for (int i = 0; i < kCols / 8; ++i)
-            reinterpret_cast<uint4*>(y)[i] =
-                make_uint4(out[4 * i], out[4 * i + 1], out[4 * i + 2], out[4 * i + 3]);
+      for (int h = 0; h < kCols / 64; ++h) {
+        const int f0 = feat + 64 * h;
+        if (tok0 >= p.T || f0 >= p.N) break;
+        if (h) fetch(f0);
+        if (RES && p.vec) {
+          wait_phase(rbar, res_phase, abort_flag, p.status);
+          res_phase ^= 1u;
+        } else if (p.vec) {
+          if (lane == 0) bulk_wait_read();
+          __syncwarp();
         } else {
+          __syncwarp();
+        }
 #pragma unroll
-          for (int i = 0; i < kCols; ++i)
-            if (feat + i < p.N) y[i] = (uint16_t)(out[i / 2] >> (16 * (i & 1)));
+        for (int c = 0; c < 8; ++c) {  // 8 features
+          float v[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            v[i] = __uint_as_float(r[64 * h + 8 * c + i]);
+            const int f = f0 + 8 * c + i;
+            if (p.bias) v[i] += f < p.N ? __ldg(p.bias + f) : 0.f;
+          }
+          uint4* at = reinterpret_cast<uint4*>(my + ((c ^ (lane & 7)) << 4));
+          if (RES) {
+            const uint4 u = *at;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] += bf16x8_elem(u, i);
+          }
+          uint4 o;
+          o.x = f32_to_bf16_rn(v[0]) | (uint32_t)f32_to_bf16_rn(v[1]) << 16;
+          o.y = f32_to_bf16_rn(v[2]) | (uint32_t)f32_to_bf16_rn(v[3]) << 16;
+          o.z = f32_to_bf16_rn(v[4]) | (uint32_t)f32_to_bf16_rn(v[5]) << 16;
+          o.w = f32_to_bf16_rn(v[6]) | (uint32_t)f32_to_bf16_rn(v[7]) << 16;
+          *at = o;
+        }
+        if (p.vec) {
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) tma_store_2d(&tm_y, box, f0, tok0);  // rows and columns beyond y are cut
+        } else {
+          __syncwarp();
+          for (int i = 0; i < 32 && tok0 + i < p.T; ++i)
+            for (int e = lane; e < 64 && f0 + e < p.N; e += 32)
+              p.y[(int64_t)(tok0 + i) * p.y_stride + f0 + e] = *reinterpret_cast<const uint16_t*>(
+                  box + i * 128 + (((e >> 3) ^ (i & 7)) << 4) + (e & 7) * 2);
+          __syncwarp();
         }
       }
     }
+    if (p.vec && lane == 0) bulk_wait_all();
   }
   __syncwarp();
   tc_fence_before();
@@ -254,6 +290,22 @@ cudaError_t encode_scales(CUtensorMap* m, const uint8_t* base, uint64_t blocks) 
   return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
+// [rows, cols] bf16 whose rows lie `stride` elements apart, boxes of 32 rows x 64 columns.
+cudaError_t encode_out(CUtensorMap* m, const void* base, uint64_t rows, uint64_t cols,
+                       int64_t stride) {
+  EncodeTiledFn fn = encode_fn();
+  if (!fn) return cudaErrorNotSupported;
+  const cuuint64_t dims[2] = {cols, rows};
+  const cuuint64_t strides[1] = {(cuuint64_t)stride * 2};
+  const cuuint32_t box[2] = {64, 32};
+  const cuuint32_t estr[2] = {1, 1};
+  const CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims,
+                        strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                        CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
 template <int BN, int STAGES, bool RES>
 cudaError_t launch_bn(const LinParams& p, const uint8_t* codes, const uint8_t* w,
                       cudaStream_t st) {
@@ -266,6 +318,12 @@ cudaError_t launch_bn(const LinParams& p, const uint8_t* codes, const uint8_t* w
   if (e == cudaSuccess) e = encode_scales(&mxs, p.x_scales, (uint64_t)((p.T + 127) / 128) * p.chunks);
   if (e == cudaSuccess) e = encode_scales(&mws, p.w_scales, (uint64_t)((p.N + 127) / 128) * p.chunks);
   if (e != cudaSuccess) return e;
+  CUtensorMap my = mx, mr = mx;  // not used where the rows do not suit a tensor map
+  if (p.vec) {
+    e = encode_out(&my, p.y, p.T, p.N, p.y_stride);
+    if (e == cudaSuccess && RES) e = encode_out(&mr, p.residual, p.T, p.N, p.r_stride);
+    if (e != cudaSuccess) return e;
+  }
   auto kern = k_mx_linear_pair<BN, STAGES, RES>;
   e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)S::kTotal);
   if (e != cudaSuccess) return e;
@@ -274,23 +332,26 @@ cudaError_t launch_bn(const LinParams& p, const uint8_t* codes, const uint8_t* w
   const long pairs = num_sms() / 2;
   count_launches(1);
   return launch_pdl_cluster(kern, dim3((unsigned)(2 * (total < pairs ? total : pairs))),
-                            dim3(kPairThreads), S::kTotal, st, 2u, mx, mw, mxs, mws, p, ttiles,
-                            ftiles);
+                            dim3(kPairThreads), S::kTotal, st, 2u, mx, mw, mxs, mws, my, mr, p,
+                            ttiles, ftiles);
 }
 
 }  // namespace
 
 cudaError_t launch_pair(const LinParams& p, const uint8_t* codes, const uint8_t* w,
                         cudaStream_t st) {
-  // 256 features a tile, or 128 where that makes the longest pair's share of tiles shorter
+  // 256 features a tile, or 128 where that makes the longest pair's share of tiles shorter. A tile's
+  // time in stages of 256 features' (496 cycles): 0.87 a stage with 128 (the tokens' side bounds the MMAs),
+  // and its ends
   const long pairs = num_sms() / 2, tt = (p.T + 255) / 256;
-  const long n256 = (tt * ((p.N + 255) / 256) + pairs - 1) / pairs * 2;
-  const long n128 = (tt * ((p.N + 127) / 128) + pairs - 1) / pairs;
-  if (n128 < n256)
+  const float nst = (float)((p.chunks + 1) / 2);
+  const float t256 = (float)((tt * ((p.N + 255) / 256) + pairs - 1) / pairs) * (nst + 5.f);
+  const float t128 = (float)((tt * ((p.N + 127) / 128) + pairs - 1) / pairs) * (0.87f * nst + 3.f);
+  if (t128 < t256)
     return p.residual ? launch_bn<128, 7, true>(p, codes, w, st)
                       : launch_bn<128, 7, false>(p, codes, w, st);
-  return p.residual ? launch_bn<256, 6, true>(p, codes, w, st)
-                    : launch_bn<256, 6, false>(p, codes, w, st);
+  return p.residual ? launch_bn<256, 5, true>(p, codes, w, st)
+                    : launch_bn<256, 5, false>(p, codes, w, st);
 }
 
 }  // namespace mxl
