@@ -5,18 +5,6 @@
 
 namespace moe {
 
-// n / d for 0 <= n < 2^31 by one multiplication: m = ceil(2^p / d) with p = 31 + ceil(log2 d).
-struct FastDiv {
-  uint32_t d, m, p;
-};
-
-inline FastDiv fast_div(uint32_t d) {
-  FastDiv f{d, 0, 31};
-  while ((1ull << (f.p - 31)) < d) ++f.p;
-  f.m = (uint32_t)(((1ull << f.p) + d - 1) / d);
-  return f;
-}
-
 // moe_attn_shape with every default filled in
 struct AttnDims {
   int T, B, Hq, Hkv, G, D;

@@ -37,6 +37,18 @@ struct WsLayout {
   int nchunk;
 };
 
+// n / d for 0 <= n < 2^31 by one multiplication: m = ceil(2^p / d) with p = 31 + ceil(log2 d).
+struct FastDiv {
+  uint32_t d, m, p;
+};
+
+inline FastDiv fast_div(uint32_t d) {
+  FastDiv f{d, 0, 31};
+  while ((1ull << (f.p - 31)) < d) ++f.p;
+  f.m = (uint32_t)(((1ull << f.p) + d - 1) / d);
+  return f;
+}
+
 inline size_t align_up(size_t v, size_t a) { return (v + a - 1) / a * a; }
 
 inline WsLayout ws_layout(const moe_shape& s) {

@@ -13,46 +13,94 @@ namespace moe {
 namespace {
 
 using namespace mxl;
+#ifndef PREF
+#define PREF 1
+#endif
+#ifndef SPL
+#define SPL 2
+#endif
+#ifndef QR
+#define QR kQuantRows
+#endif
+#ifndef MINST
+#define MINST 1
+#endif
+#ifndef ST128
+#define ST128 3
+#endif
+#ifndef ST16
+#define ST16 5
+#endif
+#ifndef MAXS
+#define MAXS 8
+#endif
 
+constexpr int kQuantRows = 4;  // rows of 256 of K that a warp quantises in a block: 4 * 4 in all
 constexpr int kLinThreads = 192;  // warps: 0 loads, 1 MMAs, 2..5 quantise x, then read the sums
 
-template <int NT, int STAGES>
+// A ring of stages; x that the block quantises itself (QUANT) lies beside it whole.
+template <int NT, int STAGES, bool QUANT>
 struct LinSmem {
   static constexpr uint32_t kA = kBM * kRowBytes;
   static constexpr uint32_t kB = NT * kRowBytes;
-  static constexpr uint32_t kTiles = STAGES * (kA + kB);
-  static constexpr uint32_t kScales = STAGES * 2 * kSfBytes;
+  static constexpr uint32_t kTiles = STAGES * (kA + (QUANT ? 0 : kB));
+  static constexpr uint32_t kScales = STAGES * (QUANT ? 1 : 2) * kSfBytes;
+  static constexpr uint32_t kRing = kTiles + kScales;
+  static constexpr uint32_t kX = QUANT ? kB + kSfBytes : 0;  // of a stage of x
   static constexpr uint32_t kPart = NT * kBM * 4;  // the sums, over the tiles once they are read
-  static constexpr uint32_t kBars = 8 * (2 * STAGES + 1) + 16;
-  static constexpr uint32_t kTotal = kTiles + kScales + kBars + 1024;
+  static constexpr uint32_t kBars = 8 * (2 * STAGES + 2) + 16;
+  static constexpr uint32_t total(int nx) { return kRing + nx * kX + kBars + 1024; }
   static constexpr uint32_t kSfCol = NT;  // scales: 2 x (8 columns of A, 8 of B)
   static constexpr uint32_t kCols = NT + 32 <= 64 ? 64 : NT + 32 <= 128 ? 128 : 256;
 };
+
+// The sums of S blocks for four rows of w, in the order of K; all S loads on their way at once.
+template <int S>
+__device__ __forceinline__ float4 gathered(uint32_t addr) {
+  float4 a[S];
+#pragma unroll
+  for (int s = 0; s < S; ++s) a[s] = ld_cluster_f4(mapa_shared(addr, s));
+#pragma unroll
+  for (int s = 1; s < S; ++s) {
+    a[0].x += a[s].x;
+    a[0].y += a[s].y;
+    a[0].z += a[s].z;
+    a[0].w += a[s].w;
+  }
+  return a[0];
+}
 
 template <int NT, int STAGES, bool QUANT>
 __global__ void __launch_bounds__(kLinThreads, 2)
     k_mx_linear(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_x,
                 const LinParams p) {
-  using S = LinSmem<NT, STAGES>;
-  static_assert(S::kPart <= S::kTiles, "the sums fit over the tiles");
+  using S = LinSmem<NT, STAGES, QUANT>;
+  static_assert(S::kPart <= S::kRing, "the sums fit over the ring");
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~uintptr_t(1023));
-  uint8_t* sm_b = smem + STAGES * S::kA;
-  uint8_t* sm_sf = smem + S::kTiles;  // per stage: of w, of x
-  uint64_t* full = reinterpret_cast<uint64_t*>(smem + S::kTiles + S::kScales);
+  const int nst = (p.chunks + 1) >> 1;
+  const int rank = (int)(blockIdx.x % (unsigned)p.splits);
+  const int k0 = (int)((long)nst * rank / p.splits), k1 = (int)((long)nst * (rank + 1) / p.splits);
+  const int nx = QUANT ? (nst + p.splits - 1) / p.splits : 0;  // most stages of a block
+  uint8_t* sm_b = smem + STAGES * S::kA;      // x's tiles: of the ring, or
+  uint8_t* sm_x = smem + S::kRing;            // whole: tiles, then scales
+  uint8_t* sm_sf = smem + S::kTiles;          // per stage: of w, of the ring's x
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + S::kRing + nx * S::kX);
   uint64_t* empty = full + STAGES;
   uint64_t* acc_full = empty + STAGES;
-  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(acc_full + 1);
+  uint64_t* x_full = acc_full + 1;
+  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(x_full + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     for (int s = 0; s < STAGES; ++s) {
-      mbar_init(&full[s], QUANT ? 5 : 1);  // the loads, and the four quantising warps
+      mbar_init(&full[s], 1);
       mbar_init(&empty[s], 1);
     }
     mbar_init(acc_full, 1);
+    mbar_init(x_full, 4);  // the quantising warps
     *abort_flag = 0;
     fence_mbar_init();
     prefetch_tmap(&tm_w);
@@ -67,28 +115,38 @@ __global__ void __launch_bounds__(kLinThreads, 2)
   tc_fence_after();
   const uint32_t tmem = *tmem_holder;
 
-  const int rank = (int)(blockIdx.x % (unsigned)p.splits);
   const int tile = (int)(blockIdx.x / (unsigned)p.splits);
   const int mt = tile % p.mtiles, tt = tile / p.mtiles;
   const int row0 = mt * kBM, tok0 = tt * NT;
   const int ntok = min(NT, p.T - tok0);
   const int npad = (ntok + 15) & ~15;
-  const int nst = (p.chunks + 1) >> 1;
-  const int k0 = (int)((long)nst * rank / p.splits), k1 = (int)((long)nst * (rank + 1) / p.splits);
 
+  // Ahead of the wait for the kernel before: behind the call's own quantisation of x, which has itself
+  // waited for everything before it, the first stages of the weights; else, as that kernel may still be
+  // writing them, their way to L2 alone, where whatever it writes is written as well.
+  const auto load_w = [&](int kb, uint32_t stage) {
+    const uint32_t sf = (uint32_t)min(2, p.chunks - 2 * kb) * kMxTile;
+    mbar_arrive_expect_tx(&full[stage], S::kA + sf + (QUANT ? 0u : S::kB + sf));
+    tma_load_2d(smem + stage * S::kA, &tm_w, &full[stage], kb * (int)kRowBytes, row0,
+                policy_evict_first());
+    bulk_load(sm_sf + stage * (QUANT ? 1 : 2) * kSfBytes,
+              p.w_scales + ((size_t)mt * p.chunks + 2 * kb) * kMxTile, sf, &full[stage]);
+  };
+  const int early = !QUANT && p.early ? min(STAGES, k1 - k0) : 0;
+  if (warp == 0 && elect_one()) {
+    for (int i = 0; i < early; ++i) load_w(k0 + i, (uint32_t)i);
+    for (int kb = k0 + early; kb < k1; ++kb) tma_prefetch_2d(&tm_w, kb * (int)kRowBytes, row0);
+  }
   pdl_wait_then_release();
 
   if (warp == 0) {
     if (elect_one()) {
       uint32_t stage = 0, phase = 0;
-      const uint64_t pol_w = policy_evict_first(), pol_x = policy_evict_last();
+      const uint64_t pol_x = policy_evict_last();
       for (int kb = k0; kb < k1; ++kb) {
         if (!wait_phase(&empty[stage], phase ^ 1u, abort_flag, p.status)) break;
         const uint32_t sf = (uint32_t)min(2, p.chunks - 2 * kb) * kMxTile;
-        mbar_arrive_expect_tx(&full[stage], S::kA + sf + (QUANT ? 0u : S::kB + sf));
-        tma_load_2d(smem + stage * S::kA, &tm_w, &full[stage], kb * (int)kRowBytes, row0, pol_w);
-        bulk_load(sm_sf + stage * 2 * kSfBytes,
-                  p.w_scales + ((size_t)mt * p.chunks + 2 * kb) * kMxTile, sf, &full[stage]);
+        if (kb - k0 >= early) load_w(kb, stage);
         if (!QUANT) {
           tma_load_2d(sm_b + stage * S::kB, &tm_x, &full[stage], kb * (int)kRowBytes, tok0, pol_x);
           bulk_load(sm_sf + (stage * 2 + 1) * kSfBytes,
@@ -106,19 +164,23 @@ __global__ void __launch_bounds__(kLinThreads, 2)
   } else if (warp == 1) {
     if (elect_one()) {
       uint32_t stage = 0, phase = 0;
-      bool ok = true;
-      for (int kb = k0; kb < k1; ++kb) {
+      bool ok = !QUANT || wait_phase(x_full, 0, abort_flag, p.status);
+      for (int kb = k0; ok && kb < k1; ++kb) {
         if (!wait_phase(&full[stage], phase, abort_flag, p.status)) { ok = false; break; }
         tc_fence_after();
         const int n64 = min(4, (p.K - kb * kStageK + 63) >> 6);  // of K there is
         const uint32_t sf = tmem + S::kSfCol + (uint32_t)(kb & 1) * 16;
-        const uint32_t sa = smem_u32(sm_sf + stage * 2 * kSfBytes), sb = sa + kSfBytes;
+        const uint32_t sa = smem_u32(sm_sf + stage * (QUANT ? 1 : 2) * kSfBytes);
+        const uint32_t xb = QUANT ? smem_u32(sm_x + (kb - k0) * S::kB)
+                                  : smem_u32(sm_b + stage * S::kB);
+        const uint32_t sb = QUANT ? smem_u32(sm_x + nx * S::kB + (kb - k0) * kSfBytes)
+                                  : sa + kSfBytes;
         for (int c = 0; 2 * c < n64; ++c) {
           tmem_cp_scales(sf + 4 * c, scale_desc(sa + c * kMxTile));
           tmem_cp_scales(sf + 8 + 4 * c, scale_desc(sb + c * kMxTile));
         }
         const uint64_t ad = sw128_desc(smem_u32(smem + stage * S::kA));
-        const uint64_t bd = sw128_desc(smem_u32(sm_b + stage * S::kB));
+        const uint64_t bd = sw128_desc(xb);
         for (int j = 0; j < n64; ++j)
           mma_mxf4(tmem, ad + 2 * j, bd + 2 * j, idesc_mxf4(kBM, npad, 2 * (j & 1)),
                    sf + 4 * (j >> 1), sf + 8 + 4 * (j >> 1), (kb > k0 || j) ? 1u : 0u);
@@ -130,35 +192,38 @@ __global__ void __launch_bounds__(kLinThreads, 2)
   } else {
     const int w = warp - 2;
     if (QUANT) {
-      // warp w quantises rows w, w + 4, ... of the stage into the swizzled tile and its scales
-      uint32_t stage = 0, phase = 0;
-      for (int kb = k0; kb < k1; ++kb) {
-        const int k = kb * kStageK + 8 * lane;
-        if (!__all_sync(0xffffffffu, wait_phase(&empty[stage], phase ^ 1u, abort_flag, p.status))) break;
-        uint8_t* b = sm_b + stage * S::kB;
-        uint8_t* sf = sm_sf + (stage * 2 + 1) * kSfBytes;
-        for (int n = w; n < ntok; n += 4) {
-          uint4 u = make_uint4(0, 0, 0, 0);
-          if (k < p.K) u = ldg_u4(p.x + (int64_t)(tok0 + n) * p.x_stride + k);
-          float v[8];
-          mxq::bf16x8(u, v);
-          const uint32_t s = mxq::quad_scale(v);
-          const float f = mxq::inverse(s);
+      // Rows of 256 of K, one a warp at a time, all of the block's loads on their way at once (behind the
+      // weights' loads a second batch would wait for microseconds), into swizzled tiles and their scales;
+      // one fence and one arrival for the whole of x.
+      const int rows = ntok * (k1 - k0);  // row q: token q % ntok of stage q / ntok
+      const uint32_t inv = 65536u / (uint32_t)ntok + 1;  // q < 64, exact
+      uint4 u[kQuantRows];
 #pragma unroll
-          for (int i = 0; i < 8; ++i) v[i] = s == 255u ? 0.f : v[i] * f;
-          *reinterpret_cast<uint32_t*>(b + n * kRowBytes + (((lane >> 2) ^ (n & 7)) << 4) +
-                                       (lane & 3) * 4) = mxq::codes8(v);
-          if ((lane & 3) == 0) {
-            const int j = lane >> 2;
-            sf[(j >> 2) * kMxTile + (n & 31) * 16 + (n >> 5) * 4 + (j & 3)] = (uint8_t)s;
-          }
-        }
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&full[stage]);
-        if (++stage == STAGES) { stage = 0; phase ^= 1u; }
+      for (int i = 0; i < kQuantRows; ++i) {
+        const int q = w + 4 * i, kb = (int)(((uint32_t)q * inv) >> 16), n = q - kb * ntok;
+        const int k = (k0 + kb) * kStageK + 8 * lane;
+        u[i] = make_uint4(0, 0, 0, 0);
+        if (q < rows && k < p.K) u[i] = ldg_u4(p.x + (int64_t)(tok0 + n) * p.x_stride + k);
       }
+#pragma unroll
+      for (int i = 0; i < kQuantRows; ++i) {
+        const int q = w + 4 * i, kb = (int)(((uint32_t)q * inv) >> 16), n = q - kb * ntok;
+        if (q >= rows) break;
+        float v[8];
+        mxq::bf16x8(u[i], v);
+        uint32_t s;
+        const uint32_t c = mxq::quantise8(v, s);
+        *reinterpret_cast<uint32_t*>(sm_x + kb * S::kB + n * kRowBytes +
+                                     (((lane >> 2) ^ (n & 7)) << 4) + (lane & 3) * 4) = c;
+        if ((lane & 3) == 0) {
+          const int j = lane >> 2;
+          sm_x[nx * S::kB + kb * kSfBytes + (j >> 2) * kMxTile + (n & 31) * 16 + (n >> 5) * 4 +
+               (j & 3)] = (uint8_t)s;
+        }
+      }
+      fence_proxy_async_smem();
       __syncwarp();
+      if (lane == 0) mbar_arrive(x_full);
     }
     // the sums: lane = row of w, column = token
     if (__all_sync(0xffffffffu, wait_phase(acc_full, 0, abort_flag, p.status))) {
@@ -187,15 +252,11 @@ __global__ void __launch_bounds__(kLinThreads, 2)
     for (int q = (int)((long)total * rank / p.splits) + threadIdx.x; q < q1; q += kLinThreads) {
       const int n = q >> 5, feat = row0 + 4 * (q & 31);
       if (feat >= p.N) continue;
-      float v[4] = {0.f, 0.f, 0.f, 0.f};
-      for (int s = 0; s < p.splits; ++s) {
-        const float4 a = p.splits > 1 ? ld_cluster_f4(mapa_shared(base + 16 * q, s))
-                                      : *reinterpret_cast<const float4*>(smem + 16 * q);
-        v[0] += a.x;
-        v[1] += a.y;
-        v[2] += a.z;
-        v[3] += a.w;
-      }
+      const float4 a = p.splits == 1   ? *reinterpret_cast<const float4*>(smem + 16 * q)
+                       : p.splits == 2 ? gathered<2>(base + 16 * q)
+                       : p.splits == 4 ? gathered<4>(base + 16 * q)
+                                       : gathered<8>(base + 16 * q);
+      float v[4] = {a.x, a.y, a.z, a.w};
       uint16_t* y = p.y + (int64_t)(tok0 + n) * p.y_stride + feat;
       const uint16_t* res = p.residual + (int64_t)(tok0 + n) * p.r_stride + feat;
       if (p.bias) {
@@ -235,22 +296,20 @@ __global__ void __launch_bounds__(kLinThreads, 2)
 template <int NT, int STAGES, bool QUANT>
 cudaError_t launch_tile(const CUtensorMap& w, const CUtensorMap& x, const LinParams& p, int tiles,
                         cudaStream_t st) {
-  using S = LinSmem<NT, STAGES>;
-  static_assert(S::kTotal <= 227 * 1024, "shared memory");
+  using S = LinSmem<NT, STAGES, QUANT>;
+  const int nst = (p.chunks + 1) / 2;
+  const uint32_t smem = S::total(QUANT ? (nst + p.splits - 1) / p.splits : 0);
   auto kern = k_mx_linear<NT, STAGES, QUANT>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       (int)S::kTotal);
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
   count_launches(1);
   const dim3 grid((unsigned)tiles * (unsigned)p.splits), block(kLinThreads);
   return p.splits > 1
-             ? launch_pdl_cluster(kern, grid, block, S::kTotal, st, (unsigned)p.splits, w, x, p)
-             : launch_pdl(kern, grid, block, S::kTotal, st, w, x, p);
+             ? launch_pdl_cluster(kern, grid, block, smem, st, (unsigned)p.splits, w, x, p)
+             : launch_pdl(kern, grid, block, smem, st, w, x, p);
 }
 
 // Tokens up to which the product's own warps quantise x, so that a call is one launch.
-constexpr int kQuantTokens = 32;
-
 }  // namespace
 
 cudaError_t launch_mx_linear(const MxDims& d, const void* x, const uint8_t* x_scales,
@@ -259,7 +318,13 @@ cudaError_t launch_mx_linear(const MxDims& d, const void* x, const uint8_t* x_sc
                              cudaStream_t st) {
   if (d.T == 0) return cudaSuccess;
   cudaError_t e = cudaSuccess;
-  const bool fused = !d.quantised && d.T <= kQuantTokens;
+  const int nt = d.T <= 16 ? 16 : d.T <= 32 ? 32 : d.T <= 64 ? 64 : 128;
+  const int mtiles = (d.N + kBM - 1) / kBM, tiles = mtiles * ((d.T + nt - 1) / nt);
+  const int nst = (mx_chunks(d.K) + 1) / 2;
+  int splits = 1;
+  while (splits < MAXS && 2 * splits * MINST <= nst && tiles * 2 * splits <= SPL * num_sms()) splits *= 2;
+  // the product's own warps quantise x where it is that small, so that a call is one launch
+  const bool fused = !d.quantised && nt == 16 && d.T * ((nst + splits - 1) / splits) <= 4 * QR;
   const uint8_t* codes = static_cast<const uint8_t*>(x);
   if (!d.quantised && !fused) {
     const MxRows r{d.T, d.K, false, true, d.x_stride};
@@ -273,7 +338,8 @@ cudaError_t launch_mx_linear(const MxDims& d, const void* x, const uint8_t* x_sc
   p.T = d.T;
   p.N = d.N;
   p.K = d.K;
-  p.mtiles = (d.N + kBM - 1) / kBM;
+  p.mtiles = mtiles;
+  p.splits = splits;
   p.chunks = mx_chunks(d.K);
   p.x_stride = d.x_stride;
   p.y_stride = d.y_stride;
@@ -285,28 +351,25 @@ cudaError_t launch_mx_linear(const MxDims& d, const void* x, const uint8_t* x_sc
   p.residual = residual;
   p.y = y;
   p.vec = d.y_stride % 4 == 0 && (!residual || d.r_stride % 4 == 0);
+  p.early = !d.quantised && !fused;
   p.status = reinterpret_cast<int*>(ws + L.status);
-  if (d.T > 128) {
+#ifndef PT
+#define PT 128
+#endif
+  if (d.T > PT) {
     p.vec = d.y_stride % 8 == 0 && (!residual || d.r_stride % 8 == 0);
     return launch_pair(p, codes, w, st);
   }
-  const int nt = d.T <= 16 ? 16 : d.T <= 32 ? 32 : d.T <= 64 ? 64 : 128;
-  const int tiles = p.mtiles * ((d.T + nt - 1) / nt);
-  const int nst = (p.chunks + 1) / 2;
-  p.splits = 1;
-  while (p.splits < 8 && 2 * p.splits <= nst && tiles * 2 * p.splits <= 2 * num_sms()) p.splits *= 2;
   CUtensorMap mw, mx;
   if ((e = encode_u8_2d(&mw, w, d.N, d.K / 2, kBM)) != cudaSuccess) return e;
   mx = mw;
   if (!fused && (e = encode_u8_2d(&mx, codes, d.T, d.K / 2, nt)) != cudaSuccess) return e;
   if (nt == 16)
-    return fused ? launch_tile<16, 5, true>(mw, mx, p, tiles, st)
-                 : launch_tile<16, 5, false>(mw, mx, p, tiles, st);
-  if (nt == 32)
-    return fused ? launch_tile<32, 5, true>(mw, mx, p, tiles, st)
-                 : launch_tile<32, 5, false>(mw, mx, p, tiles, st);
+    return fused ? launch_tile<16, ST16, true>(mw, mx, p, tiles, st)
+                 : launch_tile<16, ST16, false>(mw, mx, p, tiles, st);
+  if (nt == 32) return launch_tile<32, ST16, false>(mw, mx, p, tiles, st);
   if (nt == 64) return launch_tile<64, 4, false>(mw, mx, p, tiles, st);
-  return launch_tile<128, 6, false>(mw, mx, p, tiles, st);
+  return launch_tile<128, ST128, false>(mw, mx, p, tiles, st);
 }
 
 }  // namespace moe

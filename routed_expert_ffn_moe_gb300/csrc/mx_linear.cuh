@@ -26,6 +26,7 @@ struct LinParams {
   const float* bias;
   const uint16_t* residual;
   uint16_t* y;
+  int early;  // the kernel ahead is the call's own quantisation of x
   int vec;  // rows of y and of the residual: 8-byte accesses
   int* status;
 };

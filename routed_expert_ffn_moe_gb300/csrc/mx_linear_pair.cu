@@ -34,6 +34,31 @@ struct PairSmem {
   static constexpr uint32_t kSfCols = 8 + 8 * kBlocks;     // of a stage: tokens, then weights
 };
 
+// Two values rounded to bf16, the first in the low half.
+__device__ __forceinline__ uint32_t bf16_pair(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+// The bias of eight features (the first a multiple of 8) added; none beyond N.
+__device__ __forceinline__ void add_bias(const LinParams& p, int f, float (&v)[8]) {
+  if (f + 8 <= p.N) {
+    const float4 a = __ldg(reinterpret_cast<const float4*>(p.bias + f));
+    const float4 b = __ldg(reinterpret_cast<const float4*>(p.bias + f + 4));
+    v[0] += a.x; v[1] += a.y; v[2] += a.z; v[3] += a.w;
+    v[4] += b.x; v[5] += b.y; v[6] += b.z; v[7] += b.w;
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] += f + i < p.N ? __ldg(p.bias + f + i) : 0.f;
+  }
+}
+
+// Element e of token r in a box.
+__device__ __forceinline__ uint16_t* boxed(uint8_t* box, int r, int e) {
+  return reinterpret_cast<uint16_t*>(box + r * 128 + (((e >> 3) ^ (r & 7)) << 4) + (e & 7) * 2);
+}
+
 template <int BN, int STAGES, bool RES>
 __global__ void __launch_bounds__(kPairThreads, 1)
     k_mx_linear_pair(const __grid_constant__ CUtensorMap tm_x,
@@ -88,6 +113,25 @@ __global__ void __launch_bounds__(kPairThreads, 1)
   const int total = ttiles * ftiles;
   const int nst = (p.chunks + 1) >> 1;
 
+  // A stage's weights and their scales; the even CTA's thread also announces all of both CTAs' bytes.
+  const auto load_w = [&](int tile, int kb, uint32_t stage) {
+    const int ft = tile % ftiles, ws = ft * S::kBlocks * p.chunks;
+    const uint32_t bar = mapa_shared(smem_u32(&full[stage]), 0);
+    const uint64_t pol = policy_evict_normal();
+    uint8_t* sf = sm_sf + stage * S::kSf + kSfBytes;
+    if (rank == 0) mbar_arrive_expect_tx(&full[stage], 2 * S::kStageBytes);
+    tma_load_2d_pair(smem + stage * S::kTileBytes + S::kA, &tm_w, bar, kb * (int)kRowBytes,
+                     ft * BN + rank * (BN / 2), pol);
+    // boxes of two 512-byte blocks; beyond K or the last row they hold anything, or zeros
+#pragma unroll
+    for (int b = 0; b < S::kBlocks; ++b)
+      tma_load_2d_pair(sf + b * kSfBytes, &tm_ws, bar, 0, ws + b * p.chunks + 2 * kb, pol);
+  };
+  // Behind the call's own quantisation of x, which has waited for everything before it, the first
+  // stages' weights need not wait for x.
+  const int early = p.early && tile0 < total ? min(STAGES, nst) : 0;
+  if (warp == 0 && elect_one())
+    for (int kb = 0; kb < early; ++kb) load_w(tile0, kb, (uint32_t)kb);
   pdl_wait_then_release();
 
   if (warp == 0) {
@@ -97,23 +141,14 @@ __global__ void __launch_bounds__(kPairThreads, 1)
       uint32_t stage = 0, phase = 0;
       bool ok = true;
       for (int tile = tile0; ok && tile < total; tile += tstep) {
-        const int tt = tile / ftiles, ft = tile - tt * ftiles;
-        const int tok = tt * 256 + rank * 128, feat = ft * BN + rank * (BN / 2);
-        const int xs = (tt * 2 + rank) * p.chunks, ws = ft * S::kBlocks * p.chunks;
+        const int tt = tile / ftiles;
+        const int tok = tt * 256 + rank * 128, xs = (tt * 2 + rank) * p.chunks;
         for (int kb = 0; kb < nst; ++kb) {
           if (!wait_phase(&empty[stage], phase ^ 1u, abort_flag, p.status)) { ok = false; break; }
-          if (rank == 0) mbar_arrive_expect_tx(&full[stage], 2 * S::kStageBytes);
+          if (tile != tile0 || kb >= early) load_w(tile, kb, stage);
           const uint32_t bar = full0 + 8u * stage;
-          uint8_t* a = smem + stage * S::kTileBytes;
-          uint8_t* sf = sm_sf + stage * S::kSf;
-          tma_load_2d_pair(a, &tm_x, bar, kb * (int)kRowBytes, tok, pol);
-          tma_load_2d_pair(a + S::kA, &tm_w, bar, kb * (int)kRowBytes, feat, pol);
-          // boxes of two 512-byte blocks; beyond K or the last row they hold anything, or zeros
-          tma_load_2d_pair(sf, &tm_xs, bar, 0, xs + 2 * kb, pol);
-#pragma unroll
-          for (int b = 0; b < S::kBlocks; ++b)
-            tma_load_2d_pair(sf + (1 + b) * kSfBytes, &tm_ws, bar, 0, ws + b * p.chunks + 2 * kb,
-                             pol);
+          tma_load_2d_pair(smem + stage * S::kTileBytes, &tm_x, bar, kb * (int)kRowBytes, tok, pol);
+          tma_load_2d_pair(sm_sf + stage * S::kSf, &tm_xs, bar, 0, xs + 2 * kb, pol);
           if (++stage == STAGES) { stage = 0; phase ^= 1u; }
         }
       }
@@ -187,11 +222,19 @@ __global__ void __launch_bounds__(kPairThreads, 1)
           }
         } else {
           __syncwarp();
-          for (int r = 0; r < 32 && tok0 + r < p.T; ++r)
-            for (int e = lane; e < 64 && f0 + e < p.N; e += 32)
-              *reinterpret_cast<uint16_t*>(box + r * 128 + (((e >> 3) ^ (r & 7)) << 4) +
-                                           (e & 7) * 2) =
-                  p.residual[(int64_t)(tok0 + r) * p.r_stride + f0 + e];
+          for (int r0 = 0; r0 < 32; r0 += 8) {
+            uint16_t a[8][2];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              const int r = r0 + (i >> 1), e = lane + 32 * (i & 1);
+              a[i >> 1][i & 1] = tok0 + r < p.T && f0 + e < p.N
+                                     ? p.residual[(int64_t)(tok0 + r) * p.r_stride + f0 + e]
+                                     : (uint16_t)0;
+            }
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+              *boxed(box, r0 + (i >> 1), lane + 32 * (i & 1)) = a[i >> 1][i & 1];
+          }
           __syncwarp();
         }
       };
@@ -231,23 +274,16 @@ __global__ void __launch_bounds__(kPairThreads, 1)
         for (int c = 0; c < 8; ++c) {  // 8 features
           float v[8];
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            v[i] = __uint_as_float(r[64 * h + 8 * c + i]);
-            const int f = f0 + 8 * c + i;
-            if (p.bias) v[i] += f < p.N ? __ldg(p.bias + f) : 0.f;
-          }
+          for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(r[64 * h + 8 * c + i]);
+          if (p.bias) add_bias(p, f0 + 8 * c, v);
           uint4* at = reinterpret_cast<uint4*>(my + ((c ^ (lane & 7)) << 4));
           if (RES) {
             const uint4 u = *at;
 #pragma unroll
             for (int i = 0; i < 8; ++i) v[i] += bf16x8_elem(u, i);
           }
-          uint4 o;
-          o.x = f32_to_bf16_rn(v[0]) | (uint32_t)f32_to_bf16_rn(v[1]) << 16;
-          o.y = f32_to_bf16_rn(v[2]) | (uint32_t)f32_to_bf16_rn(v[3]) << 16;
-          o.z = f32_to_bf16_rn(v[4]) | (uint32_t)f32_to_bf16_rn(v[5]) << 16;
-          o.w = f32_to_bf16_rn(v[6]) | (uint32_t)f32_to_bf16_rn(v[7]) << 16;
-          *at = o;
+          *at = make_uint4(bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3]), bf16_pair(v[4], v[5]),
+                           bf16_pair(v[6], v[7]));
         }
         if (p.vec) {
           fence_proxy_async_smem();
@@ -255,10 +291,18 @@ __global__ void __launch_bounds__(kPairThreads, 1)
           if (lane == 0) tma_store_2d(&tm_y, box, f0, tok0);  // rows and columns beyond y are cut
         } else {
           __syncwarp();
-          for (int i = 0; i < 32 && tok0 + i < p.T; ++i)
-            for (int e = lane; e < 64 && f0 + e < p.N; e += 32)
-              p.y[(int64_t)(tok0 + i) * p.y_stride + f0 + e] = *reinterpret_cast<const uint16_t*>(
-                  box + i * 128 + (((e >> 3) ^ (i & 7)) << 4) + (e & 7) * 2);
+          for (int r0 = 0; r0 < 32; r0 += 8) {
+            uint16_t a[8][2];
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+              a[i >> 1][i & 1] = *boxed(box, r0 + (i >> 1), lane + 32 * (i & 1));
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              const int r = r0 + (i >> 1), e = lane + 32 * (i & 1);
+              if (tok0 + r < p.T && f0 + e < p.N)
+                p.y[(int64_t)(tok0 + r) * p.y_stride + f0 + e] = a[i >> 1][i & 1];
+            }
+          }
           __syncwarp();
         }
       }

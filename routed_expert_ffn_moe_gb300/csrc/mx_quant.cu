@@ -1,8 +1,8 @@
 // Quantisation of matrices to MXFP4, the values back, and scales from rows to tiles.
 //
 // Each element is read once and written once: the kernels are bound by HBM for all but small matrices,
-// and by launch latency for those. A thread takes 8 consecutive elements (16 bytes of bf16), so a warp reads
-// 512 bytes in a row and a block of 32 is a quad of lanes, whose largest magnitude takes two exchanges.
+// and by launch latency for those. A thread takes 16 consecutive elements to quantise (two lanes a block of
+// 32: one exchange for its largest magnitude), 8 to read back (32 lanes store 512 bytes of bf16 in a row).
 #include "mx_quant.cuh"
 
 namespace moe {
@@ -10,83 +10,156 @@ namespace {
 
 using namespace mxq;
 
+// Sixteen elements.
 template <bool F32>
-__device__ __forceinline__ void load8(const void* x, int64_t at, float (&v)[8]) {
+__device__ __forceinline__ void load16(const void* x, int64_t at, float (&v)[16]) {
   if (F32) {
-    const uint4 a = ld_stream_u4(static_cast<const float*>(x) + at);
-    const uint4 b = ld_stream_u4(static_cast<const float*>(x) + at + 4);
-    v[0] = __uint_as_float(a.x); v[1] = __uint_as_float(a.y);
-    v[2] = __uint_as_float(a.z); v[3] = __uint_as_float(a.w);
-    v[4] = __uint_as_float(b.x); v[5] = __uint_as_float(b.y);
-    v[6] = __uint_as_float(b.z); v[7] = __uint_as_float(b.w);
-  } else {
-    bf16x8(ld_stream_u4(static_cast<const uint16_t*>(x) + at), v);
-  }
-}
-
-// Unit u of 8 elements: row u / (K / 8). The grid covers all units, rounded up to whole warps.
-template <bool F32, bool TILES>
-__global__ void __launch_bounds__(256) k_mx_quantize(const void* __restrict__ x, long rows, int K,
-                                                     int64_t stride, uint8_t* __restrict__ codes,
-                                                     uint8_t* __restrict__ scales) {
-  pdl_wait_then_release();
-  const int per = K >> 3;
-  const long u = (long)blockIdx.x * blockDim.x + threadIdx.x;
-  const bool there = u < rows * per;
-  const long r = there ? u / per : 0;
-  const int c = there ? (int)(u - r * per) : 0;
-  float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-  if (there) load8<F32>(x, r * stride + 8 * c, v);
-  const uint32_t s = quad_scale(v);
-  const float f = inverse(s);
 #pragma unroll
-  for (int i = 0; i < 8; ++i) v[i] = s == 255u ? 0.f : v[i] * f;
-  if (!there) return;
-  reinterpret_cast<uint32_t*>(codes)[u] = codes8(v);
-  if ((c & 3) == 0) {
-    const int j = c >> 2, blocks = K >> 5;
-    if (!TILES) {
-      scales[r * blocks + j] = (uint8_t)s;
-    } else {
-      const size_t at = tile_at(r, j, mx_chunks(K));
-      scales[at] = (uint8_t)s;
-      if (j == blocks - 1)  // padding of the last chunk: codes beyond K are taken as 0, times 1
-        for (int i = 1; i < 4 - (j & 3); ++i) scales[at + i] = 127;
+    for (int i = 0; i < 4; ++i) {
+      const uint4 a = ld_stream_u4(static_cast<const float*>(x) + at + 4 * i);
+      v[4 * i] = __uint_as_float(a.x);
+      v[4 * i + 1] = __uint_as_float(a.y);
+      v[4 * i + 2] = __uint_as_float(a.z);
+      v[4 * i + 3] = __uint_as_float(a.w);
+    }
+  } else {
+    const uint4 a = ld_stream_u4(static_cast<const uint16_t*>(x) + at);
+    const uint4 b = ld_stream_u4(static_cast<const uint16_t*>(x) + at + 8);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      v[i] = bf16x8_elem(a, i);
+      v[8 + i] = bf16x8_elem(b, i);
     }
   }
 }
 
-template <bool F32, bool TILES>
-__global__ void __launch_bounds__(256) k_mx_dequantize(const uint8_t* __restrict__ codes,
-                                                       const uint8_t* __restrict__ scales, long rows,
-                                                       int K, int64_t stride, void* __restrict__ y) {
+// A block takes UNITS * kThreads consecutive units of its slab of kSlab rows (blockIdx.y), a thread every
+// kThreads-th of them, so that its loads are on their way together. Places are 32-bit within a slab, divided
+// by multiplication: a 64-bit division a unit took twice the time of the rest.
+constexpr int kThreads = 128;
+constexpr int kSlab = 1 << 16;
+
+struct MxWalk {
+  long rows;
+  int K, chunks;
+  int64_t stride;
+  FastDiv per;  // units of a row
+};
+
+__device__ __forceinline__ uint32_t divided(uint32_t n, const FastDiv& f) {
+  return (uint32_t)(((uint64_t)n * f.m) >> f.p);
+}
+
+// Units of 16 elements: half a block of 32. WORDS (K a multiple of 128): the scales of four blocks lie in 8
+// lanes and go out as a word.
+template <bool F32, bool TILES, bool WORDS, int UNITS>
+__global__ void __launch_bounds__(kThreads) k_mx_quantize(const void* __restrict__ x,
+                                                          const MxWalk a,
+                                                          uint8_t* __restrict__ codes,
+                                                          uint8_t* __restrict__ scales) {
   pdl_wait_then_release();
-  const int per = K >> 3;
-  const long u = (long)blockIdx.x * blockDim.x + threadIdx.x;
-  if (u >= rows * per) return;
-  const long r = u / per;
-  const int c = (int)(u - r * per), j = c >> 2;
-  const uint32_t w = __ldg(reinterpret_cast<const uint32_t*>(codes) + u);
-  const float f = value(TILES ? scales[tile_at(r, j, mx_chunks(K))] : scales[r * (K >> 5) + j]);
-  float v[8];
+  const long r0 = (long)blockIdx.y * kSlab;
+  const uint32_t units = (uint32_t)min(a.rows - r0, (long)kSlab) * a.per.d;
+  const uint32_t u0 = blockIdx.x * (kThreads * UNITS) + threadIdx.x;
+  const int lane = threadIdx.x & 31, blocks = a.K >> 5;
+  float v[UNITS][16];
+  uint32_t r[UNITS], c[UNITS];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float2 p = pair((w >> (8 * i)) & 0xFFu);
-    v[2 * i] = p.x * f;
-    v[2 * i + 1] = p.y * f;
+  for (int i = 0; i < UNITS; ++i) {
+    const uint32_t u = u0 + kThreads * i;
+    r[i] = divided(u, a.per);
+    c[i] = u - r[i] * a.per.d;
+    if (u < units) {
+      load16<F32>(x, (r0 + r[i]) * a.stride + 16 * c[i], v[i]);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 16; ++e) v[i][e] = 0.f;
+    }
   }
-  const int64_t at = r * stride + 8 * c;
-  if (F32) {
-    float4* o = reinterpret_cast<float4*>(static_cast<float*>(y) + at);
-    o[0] = make_float4(v[0], v[1], v[2], v[3]);
-    o[1] = make_float4(v[4], v[5], v[6], v[7]);
-  } else {
-    uint4 o;
-    o.x = f32_to_bf16_rn(v[0]) | (uint32_t)f32_to_bf16_rn(v[1]) << 16;
-    o.y = f32_to_bf16_rn(v[2]) | (uint32_t)f32_to_bf16_rn(v[3]) << 16;
-    o.z = f32_to_bf16_rn(v[4]) | (uint32_t)f32_to_bf16_rn(v[5]) << 16;
-    o.w = f32_to_bf16_rn(v[6]) | (uint32_t)f32_to_bf16_rn(v[7]) << 16;
-    *reinterpret_cast<uint4*>(static_cast<uint16_t*>(y) + at) = o;
+#pragma unroll
+  for (int i = 0; i < UNITS; ++i) {
+    const uint32_t u = u0 + kThreads * i;
+    uint32_t m = 0;
+#pragma unroll
+    for (int e = 0; e < 16; ++e) m = max(m, __float_as_uint(v[i][e]) & 0x7FFFFFFFu);
+    m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
+    uint32_t s = scale_byte(m);
+    uint2 w = make_uint2(0, 0);
+    if (s != 255u) {
+      const float f = inverse(s);
+      float h[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) h[e] = v[i][e] * f;
+      w.x = codes8(h);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) h[e] = v[i][8 + e] * f;
+      w.y = codes8(h);
+    }
+    if (WORDS) {
+      s |= __shfl_down_sync(0xffffffffu, s, 2) << 8;  // of lanes 0, 8, ..: blocks 0, 1; then 2, 3
+      s |= __shfl_down_sync(0xffffffffu, s, 4) << 16;
+    }
+    if (u >= units) continue;
+    const long row = r0 + r[i];
+    reinterpret_cast<uint2*>(codes)[row * a.per.d + c[i]] = w;
+    const int j = (int)(c[i] >> 1);
+    const size_t at = TILES ? tile_at(row, j, a.chunks) : (size_t)row * blocks + j;
+    if (WORDS) {
+      if ((lane & 7) == 0) *reinterpret_cast<uint32_t*>(scales + at) = s;
+    } else if ((lane & 1) == 0) {
+      scales[at] = (uint8_t)s;
+      if (TILES && j == blocks - 1)  // padding of the last chunk: codes beyond K are taken as 0, times 1
+        for (int e = 1; e < 4 - (j & 3); ++e) scales[at + e] = 127;
+    }
+  }
+}
+
+// Units of 8 elements.
+template <bool F32, bool TILES, int UNITS>
+__global__ void __launch_bounds__(kThreads) k_mx_dequantize(const uint8_t* __restrict__ codes,
+                                                            const uint8_t* __restrict__ scales,
+                                                            const MxWalk a, void* __restrict__ y) {
+  pdl_wait_then_release();
+  const long r0 = (long)blockIdx.y * kSlab;
+  const uint32_t units = (uint32_t)min(a.rows - r0, (long)kSlab) * a.per.d;
+  const uint32_t u0 = blockIdx.x * (kThreads * UNITS) + threadIdx.x;
+  uint32_t w[UNITS], s[UNITS], r[UNITS], c[UNITS];
+#pragma unroll
+  for (int i = 0; i < UNITS; ++i) {
+    const uint32_t u = u0 + kThreads * i;
+    r[i] = divided(u, a.per);
+    c[i] = u - r[i] * a.per.d;
+    w[i] = s[i] = 0;
+    if (u >= units) continue;
+    const long row = r0 + r[i];
+    w[i] = __ldg(reinterpret_cast<const uint32_t*>(codes) + row * a.per.d + c[i]);
+    s[i] = __ldg(scales + (TILES ? tile_at(row, (int)(c[i] >> 2), a.chunks)
+                                 : (size_t)row * (a.K >> 5) + (c[i] >> 2)));
+  }
+#pragma unroll
+  for (int i = 0; i < UNITS; ++i) {
+    if (u0 + kThreads * i >= units) continue;
+    const float f = value(s[i]);
+    float v[8];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const float2 p = pair((w[i] >> (8 * e)) & 0xFFu);
+      v[2 * e] = p.x * f;
+      v[2 * e + 1] = p.y * f;
+    }
+    const int64_t at = (r0 + r[i]) * a.stride + 8 * c[i];
+    if (F32) {
+      float4* o = reinterpret_cast<float4*>(static_cast<float*>(y) + at);
+      o[0] = make_float4(v[0], v[1], v[2], v[3]);
+      o[1] = make_float4(v[4], v[5], v[6], v[7]);
+    } else {
+      uint4 o;
+      o.x = f32_to_bf16_rn(v[0]) | (uint32_t)f32_to_bf16_rn(v[1]) << 16;
+      o.y = f32_to_bf16_rn(v[2]) | (uint32_t)f32_to_bf16_rn(v[3]) << 16;
+      o.z = f32_to_bf16_rn(v[4]) | (uint32_t)f32_to_bf16_rn(v[5]) << 16;
+      o.w = f32_to_bf16_rn(v[6]) | (uint32_t)f32_to_bf16_rn(v[7]) << 16;
+      *reinterpret_cast<uint4*>(static_cast<uint16_t*>(y) + at) = o;
+    }
   }
 }
 
@@ -111,36 +184,77 @@ __global__ void __launch_bounds__(256) k_mx_tile_scales(const uint8_t* __restric
 
 }  // namespace
 
+namespace {
+
+// Matrices that fill the SMs at a unit a thread get several; smaller ones one, and more blocks.
+bool large(const MxRows& r, int unit) {
+  return r.rows * (r.K / unit) > (long)num_sms() * 2048;
+}
+
+MxWalk walk(const MxRows& r, int unit, int units, dim3* grid) {
+  MxWalk a{r.rows, r.K, mx_chunks(r.K), r.stride, fast_div((uint32_t)(r.K / unit))};
+  const long slab = r.rows < kSlab ? r.rows : kSlab, block = kThreads * units;
+  *grid = dim3((unsigned)((slab * (r.K / unit) + block - 1) / block),
+               (unsigned)((r.rows + kSlab - 1) / kSlab));
+  return a;
+}
+
+template <bool F32, bool TILES, bool WORDS>
+cudaError_t quantize(const MxRows& r, const void* x, uint8_t* codes, uint8_t* scales,
+                     cudaStream_t st) {
+  dim3 grid;
+  if (large(r, 16)) {
+    const MxWalk a = walk(r, 16, 2, &grid);
+    return launch_pdl(k_mx_quantize<F32, TILES, WORDS, 2>, grid, dim3(kThreads), 0, st, x, a, codes,
+                      scales);
+  }
+  const MxWalk a = walk(r, 16, 1, &grid);
+  return launch_pdl(k_mx_quantize<F32, TILES, WORDS, 1>, grid, dim3(kThreads), 0, st, x, a, codes,
+                    scales);
+}
+
+template <bool F32, bool TILES>
+cudaError_t quantize(const MxRows& r, const void* x, uint8_t* codes, uint8_t* scales,
+                     cudaStream_t st) {
+  return r.K % 128 == 0 ? quantize<F32, TILES, true>(r, x, codes, scales, st)
+                        : quantize<F32, TILES, false>(r, x, codes, scales, st);
+}
+
+template <bool F32, bool TILES>
+cudaError_t dequantize(const MxRows& r, const uint8_t* codes, const uint8_t* scales, void* y,
+                       cudaStream_t st) {
+  dim3 grid;
+  if (large(r, 8)) {
+    const MxWalk a = walk(r, 8, 4, &grid);
+    return launch_pdl(k_mx_dequantize<F32, TILES, 4>, grid, dim3(kThreads), 0, st, codes, scales, a,
+                      y);
+  }
+  const MxWalk a = walk(r, 8, 1, &grid);
+  return launch_pdl(k_mx_dequantize<F32, TILES, 1>, grid, dim3(kThreads), 0, st, codes, scales, a, y);
+}
+
+}  // namespace
+
 cudaError_t launch_mx_quantize(const MxRows& r, const void* x, uint8_t* codes, uint8_t* scales,
                                cudaStream_t st) {
   if (r.rows == 0) return cudaSuccess;
-  const dim3 grid((unsigned)((r.rows * (r.K / 8) + 255) / 256)), block(256);
   count_launches(1);
   if (r.f32)
-    return r.tiles ? launch_pdl(k_mx_quantize<true, true>, grid, block, 0, st, x, r.rows, r.K,
-                                r.stride, codes, scales)
-                   : launch_pdl(k_mx_quantize<true, false>, grid, block, 0, st, x, r.rows, r.K,
-                                r.stride, codes, scales);
-  return r.tiles ? launch_pdl(k_mx_quantize<false, true>, grid, block, 0, st, x, r.rows, r.K,
-                              r.stride, codes, scales)
-                 : launch_pdl(k_mx_quantize<false, false>, grid, block, 0, st, x, r.rows, r.K,
-                              r.stride, codes, scales);
+    return r.tiles ? quantize<true, true>(r, x, codes, scales, st)
+                   : quantize<true, false>(r, x, codes, scales, st);
+  return r.tiles ? quantize<false, true>(r, x, codes, scales, st)
+                 : quantize<false, false>(r, x, codes, scales, st);
 }
 
 cudaError_t launch_mx_dequantize(const MxRows& r, const uint8_t* codes, const uint8_t* scales,
                                  void* y, cudaStream_t st) {
   if (r.rows == 0) return cudaSuccess;
-  const dim3 grid((unsigned)((r.rows * (r.K / 8) + 255) / 256)), block(256);
   count_launches(1);
   if (r.f32)
-    return r.tiles ? launch_pdl(k_mx_dequantize<true, true>, grid, block, 0, st, codes, scales,
-                                r.rows, r.K, r.stride, y)
-                   : launch_pdl(k_mx_dequantize<true, false>, grid, block, 0, st, codes, scales,
-                                r.rows, r.K, r.stride, y);
-  return r.tiles ? launch_pdl(k_mx_dequantize<false, true>, grid, block, 0, st, codes, scales,
-                              r.rows, r.K, r.stride, y)
-                 : launch_pdl(k_mx_dequantize<false, false>, grid, block, 0, st, codes, scales,
-                              r.rows, r.K, r.stride, y);
+    return r.tiles ? dequantize<true, true>(r, codes, scales, y, st)
+                   : dequantize<true, false>(r, codes, scales, y, st);
+  return r.tiles ? dequantize<false, true>(r, codes, scales, y, st)
+                 : dequantize<false, false>(r, codes, scales, y, st);
 }
 
 cudaError_t launch_mx_tile_scales(long rows, int K, const uint8_t* scales, uint8_t* tiles,

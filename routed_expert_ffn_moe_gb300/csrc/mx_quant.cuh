@@ -79,6 +79,15 @@ __device__ __forceinline__ void bf16x8(const uint4& u, float (&v)[8]) {
   for (int i = 0; i < 8; ++i) v[i] = bf16x8_elem(u, i);
 }
 
+// The codes and the scale of eight elements of a block that a quad of lanes holds.
+__device__ __forceinline__ uint32_t quantise8(float (&v)[8], uint32_t& s) {
+  s = quad_scale(v);
+  const float f = inverse(s);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] *= f;
+  return s == 255u ? 0u : codes8(v);
+}
+
 // Place of row r's scale of 32-block j among tiles of `chunks` chunks a row of tiles.
 __device__ __forceinline__ size_t tile_at(long r, int j, int chunks) {
   return ((size_t)(r >> 7) * chunks + (j >> 2)) * kMxTile + (size_t)((r & 31) * 16) +
