@@ -145,6 +145,52 @@ def test_softmax_with_masked_logits():
     check(l, None, 8, score="softmax", renorm=False, n_group=4, topk_group=2)
 
 
+MANY = 6147  # tokens: eight lanes each, an odd number of them
+
+
+@pytest.mark.parametrize("score", ["sigmoid", "softmax"])
+@pytest.mark.parametrize("E,G,keep,top,k", [
+    (256, 8, 4, 2, 8), (256, 1, 1, 2, 8), (256, 8, 4, 1, 6), (384, 1, 1, 2, 6), (160, 8, 3, 1, 6), (64, 4, 1, 2, 3),
+    (8, 1, 1, 2, 8), (8, 2, 1, 2, 4), (32, 8, 3, 2, 8), (16, 4, 2, 1, 1), (96, 3, 2, 2, 8), (100, 5, 2, 2, 7),
+    (128, 2, 1, 2, 8), (336, 7, 3, 2, 8), (128, 1, 1, 2, 8), (320, 1, 1, 1, 4), (12, 1, 1, 2, 8)])
+def test_many_tokens(E, G, keep, top, k, score):
+    l, b = draw(MANY, E, E + k)
+    for bias in (b, None):
+        check(l, bias, k, score=score, n_group=G, topk_group=keep, group_top=top, renorm=k != 6, scale=1.5)
+
+
+def test_many_tokens_ties_masks_and_near_choices():
+    l, b = draw(MANY, 256, 21)
+    l[:500] = np.round(l[:500] * 4) / 4
+    l[500:700, 60:] = -np.inf
+    l[700, 3] = np.nan
+    l[701] = np.nan
+    l[702, 77] = np.inf
+    l[703] = -np.inf
+    l[704] = 60.0
+    l[705] = -200.0
+    l[706] = 0
+    l[707, 255] = 3e38
+    l[708] *= 1e-42  # subnormal logits
+    one = l[900].astype(np.float64)  # every c within a rounding of one value for these
+    near = (0.75 - 1 / (1 + np.exp(-one))).astype(np.float32)
+    l[901:950] = l[900]
+    l[950:1000, 8:] = -30  # all eight from one lane's experts, or one group
+    off = b.copy()
+    off[200:] = -np.inf
+    for gate in GATES:
+        for bias in (None, b, near, off):
+            check(l, bias, 8, **gate)
+
+
+def test_a_token_by_itself_and_in_a_batch():
+    l, b = draw(MANY, 256, 22)
+    for kw in (dict(n_group=8, topk_group=4), dict(score="softmax")):
+        idx, w = run(l, b, 8, **kw)
+        i1, w1 = run(l[:7], b, 8, **kw)
+        assert (idx[:7] == i1).all() and (w[:7].view(np.int32) == w1.view(np.int32)).all()
+
+
 def test_neighbouring_memory_is_untouched():
     t = torch()
     l, b = draw(13, 60, 13)
