@@ -29,8 +29,9 @@ struct PairSmem {
   static constexpr uint32_t kSf = (1 + kBlocks) * kSfBytes;
   static constexpr uint32_t kStageBytes = kTileBytes + kSf;
   static constexpr uint32_t kOut = 8 * kOutBytes;          // a box of the output for each epilogue warp
+  static constexpr uint32_t kBias = 8 * BN / 2 * 4;        // and the bias of its features
   static constexpr uint32_t kBars = 8 * (2 * STAGES + 2 + 8) + 16;
-  static constexpr uint32_t kTotal = STAGES * kStageBytes + kOut + kBars + 1024;
+  static constexpr uint32_t kTotal = STAGES * kStageBytes + kOut + kBias + kBars + 1024;
   static constexpr uint32_t kSfCols = 8 + 8 * kBlocks;     // of a stage: tokens, then weights
 };
 
@@ -41,22 +42,72 @@ __device__ __forceinline__ uint32_t bf16_pair(float lo, float hi) {
   return r;
 }
 
-// The bias of eight features (the first a multiple of 8) added; none beyond N.
-__device__ __forceinline__ void add_bias(const LinParams& p, int f, float (&v)[8]) {
-  if (f + 8 <= p.N) {
-    const float4 a = __ldg(reinterpret_cast<const float4*>(p.bias + f));
-    const float4 b = __ldg(reinterpret_cast<const float4*>(p.bias + f + 4));
-    v[0] += a.x; v[1] += a.y; v[2] += a.z; v[3] += a.w;
-    v[4] += b.x; v[5] += b.y; v[6] += b.z; v[7] += b.w;
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] += f + i < p.N ? __ldg(p.bias + f + i) : 0.f;
-  }
-}
-
 // Element e of token r in a box.
 __device__ __forceinline__ uint16_t* boxed(uint8_t* box, int r, int e) {
   return reinterpret_cast<uint16_t*>(box + r * 128 + (((e >> 3) ^ (r & 7)) << 4) + (e & 7) * 2);
+}
+
+// A box of 32 tokens x 64 features to rows that no tensor map takes, a token at a time: words where they
+// are aligned; in a row that starts at an odd element the words are of a lane's second element and the next
+// lane's first, and the row's ends go out as single elements. Few instructions a row, and predicates instead of
+// branches: eight warps an SM wait for each of them.
+template <bool ALL>
+__device__ __forceinline__ void store_rows(const LinParams& p, uint8_t* box, int tok0, int f0,
+                                           int lane) {
+  const int rows = ALL ? 32 : min(32, p.T - tok0);
+  const int64_t step = p.y_stride * 2;
+  uint8_t* o = reinterpret_cast<uint8_t*>(p.y + (int64_t)tok0 * p.y_stride + f0 + 2 * lane);
+  const uint32_t flip = (uint32_t)p.y_stride & 1u;
+  uint32_t odd = (uint32_t)(reinterpret_cast<uintptr_t>(o) >> 1) & 1u;
+  const bool end = lane == 0 || lane == 31;
+  const uint32_t shift = lane ? 16 : 0, at = lane ? 2 : 0;  // of the single element that an end's lane has
+#pragma unroll
+  for (int r0 = 0; r0 < 32; r0 += 8) {
+    uint32_t a[8], next[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) a[i] = *reinterpret_cast<const uint32_t*>(boxed(box, r0 + i, 2 * lane));
+#pragma unroll
+    for (int i = 0; i < 8; ++i) next[i] = __shfl_down_sync(0xffffffffu, a[i], 1);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const bool there = ALL || r0 + i < rows;
+      const uint32_t w = __byte_perm(a[i], next[i], odd ? 0x5432 : 0x3210);
+      if (there && (lane < 31 || !odd)) *reinterpret_cast<uint32_t*>(o + 2 * odd) = w;
+      if (there && odd && end) *reinterpret_cast<uint16_t*>(o + at) = (uint16_t)(a[i] >> shift);
+      odd ^= flip;
+      o += step;
+    }
+  }
+}
+
+// The residual of such rows into a box, 16 loads of 32 elements at a time (aligned words and single ends, half as
+// many loads, took longer: eight rows at a time instead of these).
+__device__ __forceinline__ void load_rows(const LinParams& p, uint8_t* box, int tok0, int f0,
+                                          int lane) {
+  for (int r0 = 0; r0 < 32; r0 += 8) {
+    uint16_t a[8][2];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      const int r = r0 + (i >> 1), e = lane + 32 * (i & 1);
+      a[i >> 1][i & 1] = tok0 + r < p.T && f0 + e < p.N
+                             ? p.residual[(int64_t)(tok0 + r) * p.r_stride + f0 + e]
+                             : (uint16_t)0;
+    }
+#pragma unroll
+    for (int i = 0; i < 16; ++i) *boxed(box, r0 + (i >> 1), lane + 32 * (i & 1)) = a[i >> 1][i & 1];
+  }
+}
+
+// store_rows where fewer than 64 features are left.
+__device__ __forceinline__ void store_columns(const LinParams& p, uint8_t* box, int tok0, int f0,
+                                              int lane) {
+  const int rows = min(32, p.T - tok0), cols = p.N - f0;
+  uint16_t* o = p.y + (int64_t)tok0 * p.y_stride + f0 + 2 * lane;
+  for (int r = 0; r < rows; ++r, o += p.y_stride) {
+    const uint32_t a = *reinterpret_cast<const uint32_t*>(boxed(box, r, 2 * lane));
+    if (2 * lane < cols) o[0] = (uint16_t)a;
+    if (2 * lane + 1 < cols) o[1] = (uint16_t)(a >> 16);
+  }
 }
 
 template <int BN, int STAGES, bool RES>
@@ -75,7 +126,8 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                                              ~uintptr_t(1023));
   uint8_t* sm_out = smem + STAGES * S::kTileBytes;
   uint8_t* sm_sf = sm_out + S::kOut;
-  uint64_t* full = reinterpret_cast<uint64_t*>(sm_sf + STAGES * S::kSf);
+  float* sm_bias = reinterpret_cast<float*>(sm_sf + STAGES * S::kSf);
+  uint64_t* full = reinterpret_cast<uint64_t*>(reinterpret_cast<uint8_t*>(sm_bias) + S::kBias);
   uint64_t* empty = full + STAGES;
   uint64_t* acc_full = empty + STAGES;
   uint64_t* acc_empty = acc_full + 1;
@@ -205,6 +257,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     const uint32_t empty0 = mapa_shared(smem_u32(acc_empty), 0);
     uint8_t* box = sm_out + (warp - 2) * kOutBytes;
     uint8_t* my = box + lane * 128;
+    float* bias = sm_bias + (warp - 2) * kCols;
     uint64_t* rbar = &res_full[warp - 2];
     uint32_t acc_phase = 0, res_phase = 0;
     for (int tile = tile0; tile < total; tile += tstep) {
@@ -222,23 +275,16 @@ __global__ void __launch_bounds__(kPairThreads, 1)
           }
         } else {
           __syncwarp();
-          for (int r0 = 0; r0 < 32; r0 += 8) {
-            uint16_t a[8][2];
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              const int r = r0 + (i >> 1), e = lane + 32 * (i & 1);
-              a[i >> 1][i & 1] = tok0 + r < p.T && f0 + e < p.N
-                                     ? p.residual[(int64_t)(tok0 + r) * p.r_stride + f0 + e]
-                                     : (uint16_t)0;
-            }
-#pragma unroll
-            for (int i = 0; i < 16; ++i)
-              *boxed(box, r0 + (i >> 1), lane + 32 * (i & 1)) = a[i >> 1][i & 1];
-          }
+          load_rows(p, box, tok0, f0, lane);
           __syncwarp();
         }
       };
       fetch(feat);
+      if (p.bias) {  // to shared memory while the sums are formed
+        __syncwarp();
+        for (int i = lane; i < kCols; i += 32) bias[i] = feat + i < p.N ? __ldg(p.bias + feat + i) : 0.f;
+        __syncwarp();
+      }
       const bool ok =
           __all_sync(0xffffffffu, wait_phase(acc_full, acc_phase, abort_flag, p.status));
       if (!ok) {
@@ -275,7 +321,12 @@ __global__ void __launch_bounds__(kPairThreads, 1)
           float v[8];
 #pragma unroll
           for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(r[64 * h + 8 * c + i]);
-          if (p.bias) add_bias(p, f0 + 8 * c, v);
+          if (p.bias) {
+            const float4 a = *reinterpret_cast<const float4*>(bias + 64 * h + 8 * c);
+            const float4 b = *reinterpret_cast<const float4*>(bias + 64 * h + 8 * c + 4);
+            v[0] += a.x; v[1] += a.y; v[2] += a.z; v[3] += a.w;
+            v[4] += b.x; v[5] += b.y; v[6] += b.z; v[7] += b.w;
+          }
           uint4* at = reinterpret_cast<uint4*>(my + ((c ^ (lane & 7)) << 4));
           if (RES) {
             const uint4 u = *at;
@@ -291,18 +342,9 @@ __global__ void __launch_bounds__(kPairThreads, 1)
           if (lane == 0) tma_store_2d(&tm_y, box, f0, tok0);  // rows and columns beyond y are cut
         } else {
           __syncwarp();
-          for (int r0 = 0; r0 < 32; r0 += 8) {
-            uint16_t a[8][2];
-#pragma unroll
-            for (int i = 0; i < 16; ++i)
-              a[i >> 1][i & 1] = *boxed(box, r0 + (i >> 1), lane + 32 * (i & 1));
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              const int r = r0 + (i >> 1), e = lane + 32 * (i & 1);
-              if (tok0 + r < p.T && f0 + e < p.N)
-                p.y[(int64_t)(tok0 + r) * p.y_stride + f0 + e] = a[i >> 1][i & 1];
-            }
-          }
+          if (f0 + 64 > p.N) store_columns(p, box, tok0, f0, lane);
+          else if (tok0 + 32 <= p.T) store_rows<true>(p, box, tok0, f0, lane);
+          else store_rows<false>(p, box, tok0, f0, lane);
           __syncwarp();
         }
       }

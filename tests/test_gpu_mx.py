@@ -253,6 +253,10 @@ def test_full_sizes():
     product(256, 9216, 7168, "mxfp4")
     product(1003, 4099, 2080, bias=True)
     product(2500, 2304, 1792, bias=True, residual=True)
+    product(777, 1021, 640, bias=True, residual=True)
+    product(777, 1021, 640, rs=1022, ys=1024, residual=True)
+    product(777, 1022, 640, rs=1023, ys=1029, residual=True)
+    product(777, 1022, 640, ys=1027, residual=True, alias=True)
     product(4096, 1024, 7168)
 
 
