@@ -15,6 +15,9 @@ namespace {
 using namespace mxl;
 
 constexpr int kQuantRows = 4;  // rows of 256 of K that a warp quantises in a block: 4 * 4 in all
+// Stages whose weights are on their way to L2 before the wait for the kernel ahead: 4 take one token of 9216 x
+// 7168 from 8.0 to 7.3 us; 28, a long row whole, is more than L2 holds over all blocks (65536 x 7168: 50 us for 40).
+constexpr int kAheadStages = 4;
 constexpr int kLinThreads = 192;  // warps: 0 loads, 1 MMAs, 2..5 quantise x, then read the sums
 
 // A ring of stages; x that the block quantises itself (QUANT) lies beside it whole.
@@ -114,7 +117,8 @@ __global__ void __launch_bounds__(kLinThreads, 2)
   const int early = !QUANT && p.early ? min(STAGES, k1 - k0) : 0;
   if (warp == 0 && elect_one()) {
     for (int i = 0; i < early; ++i) load_w(k0 + i, (uint32_t)i);
-    for (int kb = k0 + early; kb < k1; ++kb) tma_prefetch_2d(&tm_w, kb * (int)kRowBytes, row0);
+    for (int kb = k0 + early; kb < min(k1, k0 + kAheadStages); ++kb)
+      tma_prefetch_2d(&tm_w, kb * (int)kRowBytes, row0);
   }
   pdl_wait_then_release();
 
@@ -312,7 +316,8 @@ cudaError_t launch_mx_linear(const MxDims& d, const void* x, const uint8_t* x_sc
   // The product's own warps quantise x where it is that small, so that a call is one launch: one token of
   // 7168 x 7168 7.0 us against 8.1 with a launch ahead; 8 tokens 9.7 against 8.1, as every block quantises its
   // part of x for itself.
-  const bool fused = !d.quantised && nt == 16 && d.T * ((nst + splits - 1) / splits) <= 4 * kQuantRows;
+  const int nx = (nst + splits - 1) / splits;
+  const bool fused = !d.quantised && nt == 16 && nx <= 12 && d.T * nx <= 4 * kQuantRows;
   const uint8_t* codes = static_cast<const uint8_t*>(x);
   if (!d.quantised && !fused) {
     const MxRows r{d.T, d.K, false, true, d.x_stride};
