@@ -182,8 +182,13 @@ __global__ void __launch_bounds__(kPairThreads, 1)
   // Behind the call's own quantisation of x, which has waited for everything before it, the first
   // stages' weights need not wait for x.
   const int early = p.early && tile0 < total ? min(STAGES, nst) : 0;
-  if (warp == 0 && elect_one())
+  // (Without it, the first stages' way to L2 alone: what the kernel ahead still writes is written there.)
+  if (warp == 0 && elect_one() && tile0 < total) {
     for (int kb = 0; kb < early; ++kb) load_w(tile0, kb, (uint32_t)kb);
+    const int feat = tile0 % ftiles * BN + rank * (BN / 2);
+    for (int kb = early; kb < min(STAGES, nst); ++kb)
+      tma_prefetch_2d(&tm_w, kb * (int)kRowBytes, feat);
+  }
   pdl_wait_then_release();
 
   if (warp == 0) {

@@ -10,13 +10,12 @@
 // without a bias the key is the logit itself, whose order is that of its score.
 //
 // Choices next to a border. With a bias (and for sums of two scores) fp32 values may be ordered
-// otherwise than the formulas' values. Each fp32 c lies within delta + 2^-23 |c| of its formula:
-// sigmoid as e / (1 + e) or 1 / (1 + e), e = expf(-|l|) to 2 ulp: relative 2^-22 + 2 * 2^-24, s <= 1, so
-// delta = 2^-21; softmax: the rounding of l - max (2^-24 |l - max|, and x exp(-x) < 0.37), expf, and a
-// sum of at most 69 roundings: below 2^-17 of the largest score, 1 / Z. Neighbours in the order whose
-// difference is not above the sum of their bounds are computed in 64 bits and ordered again: about one
-// token in a thousand at 256 experts with normal logits. Equal logits with equal biases
-// (logits that were rounded to few bits) are exact ties and need no 64 bits.
+// otherwise than the formulas' values. Each fp32 c lies within delta + 2^-23 |c| of its formula: delta = 2^-20
+// for a sigmoid (order_score and its 1 + e); for softmax the rounding of l - max (2^-24 |l - max|), the
+// exponential, and a sum of at most 69 roundings: below 2^-17 of the largest score, 1 / Z. Neighbours in the order
+// whose difference is not above the sum of their bounds are computed in 64 bits and ordered again: about two
+// tokens in a thousand at 256 experts with normal logits. Equal logits with equal biases (logits that were
+// rounded to few bits) are exact ties and need no 64 bits.
 #include "internal.h"
 #include "router_gate.h"
 #include "topk.cuh"
@@ -42,6 +41,19 @@ __device__ __forceinline__ double rank_value64(uint64_t key) {
   return __longlong_as_double((long long)((key >> 63) ? (key & 0x7FFFFFFFFFFFFFFFull) : ~key));
 }
 
+__device__ __forceinline__ float rcp_approx(float x) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+
+// Scores for the order alone, without branches: __expf is off by 2 + 1.173 |x| ulp (and x exp(-x) < 0.37), the
+// reciprocal by one: a sigmoid by less than 2^-21.
+__device__ __forceinline__ float order_score(bool sigmoid, float l, float lmax, float rZ) {
+  return sigmoid ? rcp_approx(1.f + __expf(-l)) : __expf(l - lmax) * rZ;
+}
+
+// Scores for the weights.
 __device__ __forceinline__ float sigmoid32(float l) {
   const float e = expf(-fabsf(l));
   return (l < 0.f ? e : 1.f) / (1.f + e);
@@ -201,16 +213,16 @@ __device__ __noinline__ int chosen_in_64(const Token<MAXM, VEC>& t, bool kept, i
 }
 
 // A lane's experts still to be taken. Up to 8: sorted once as key << 32 | ~expert by a 19-comparator
-// network. More: the keys as they are, the best found again after each win.
+// network. More than 16: the keys as they are, the best found again after each win.
 template <int MAXM, bool VEC>
 struct Offers {
   uint64_t v[8];
-  __device__ __forceinline__ void make(const uint32_t (&key)[MAXM], const Lane<VEC>& la) {
+  __device__ __forceinline__ void make(const uint32_t (&key)[MAXM], const Lane<VEC>& la, int m0 = 0) {
 #pragma unroll
-    for (int m = 0; m < 8; ++m)
-      v[m] = m < MAXM && key[m < MAXM ? m : 0]
-                 ? ((uint64_t)key[m < MAXM ? m : 0] << 32) | (uint32_t)~(la.first + la.at(m))
-                 : 0ull;
+    for (int i = 0; i < 8; ++i) {
+      const int m = m0 + i < MAXM ? m0 + i : 0;
+      v[i] = m0 + i < MAXM && key[m] ? ((uint64_t)key[m] << 32) | (uint32_t)~(la.first + la.at(m)) : 0ull;
+    }
     auto cx = [&](int a, int b) {
       const uint64_t hi = v[a] > v[b] ? v[a] : v[b];
       const uint64_t lo = v[a] > v[b] ? v[b] : v[a];
@@ -263,10 +275,30 @@ struct OffersScan {
   }
 };
 
-template <bool SMALL, int MAXM, bool VEC>
+// Up to 16: two sorted lists, the larger head of which is offered.
+template <int MAXM, bool VEC>
+struct OffersTwo {
+  Offers<MAXM, VEC> a, b;
+  __device__ __forceinline__ void make(const uint32_t (&key)[MAXM], const Lane<VEC>& la) {
+    a.make(key, la, 0);
+    b.make(key, la, 8);
+  }
+  __device__ __forceinline__ bool first() const { return a.v[0] >= b.v[0]; }
+  __device__ __forceinline__ uint32_t best_key() const { return first() ? a.best_key() : b.best_key(); }
+  __device__ __forceinline__ int best() const { return first() ? a.best() : b.best(); }
+  __device__ __forceinline__ void pop(bool mine, const Lane<VEC>& la) {
+    const bool f = first();
+    a.pop(mine && f, la);
+    b.pop(mine && !f, la);
+  }
+};
+
+template <int LISTS, int MAXM, bool VEC>
 struct Pick { using type = OffersScan<MAXM, VEC>; };
 template <int MAXM, bool VEC>
-struct Pick<true, MAXM, VEC> { using type = Offers<MAXM, VEC>; };
+struct Pick<1, MAXM, VEC> { using type = Offers<MAXM, VEC>; };
+template <int MAXM, bool VEC>
+struct Pick<2, MAXM, VEC> { using type = OffersTwo<MAXM, VEC>; };
 
 // The warp's largest key and its expert (the lowest of equal keys), taken from its lane.
 template <typename O, bool VEC>
@@ -322,9 +354,24 @@ __device__ __forceinline__ void select_token(const GateParams& q, long tok) {
       l[m] = there ? lt[la.first + la.at(m)] : -INFINITY;
     }
   }
+  float bias[MAXM];  // loaded with the logits: one by one where they are used, each would wait for its own
+#pragma unroll
+  for (int m = 0; m < MAXM; m += VEC ? 4 : 1) {
+    const bool there = q.bias && la.in && la.at(m) < q.per;
+    if (VEC) {
+      float4 f = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (there) f = __ldg(reinterpret_cast<const float4*>(q.bias + la.first + la.at(m)));
+      bias[m] = f.x;
+      bias[m + 1] = f.y;
+      bias[m + 2] = f.z;
+      bias[m + 3] = f.w;
+    } else {
+      bias[m] = there ? __ldg(q.bias + la.first + la.at(m)) : 0.f;
+    }
+  }
   const bool sums = q.keep < q.G && q.group_top == 2;  // group values are sums of scores
   const bool need_c = q.bias || sums;
-  float lmax = 0.f, Z = 1.f, delta = 4.76837158e-7f;  // 2^-21
+  float lmax = 0.f, Z = 1.f, delta = 9.53674316e-7f;  // 2^-20
   if (!q.sigmoid && (need_c || !q.renorm)) {
     float mx = -INFINITY;
 #pragma unroll
@@ -340,6 +387,7 @@ __device__ __forceinline__ void select_token(const GateParams& q, long tok) {
     delta = 7.62939453e-6f / Z;  // 2^-17 of the largest score
   }
 
+  const float rZ = rcp_approx(Z);
   // keys: of c with a bias, else of the logit; t1, t2: the lane's largest two c
   uint32_t key[MAXM], t1 = 0, t2 = 0;
 #pragma unroll
@@ -348,8 +396,8 @@ __device__ __forceinline__ void select_token(const GateParams& q, long tok) {
     key[m] = there ? rank_key(l[m]) : 0u;
     uint32_t ck = key[m];
     if (need_c) {
-      float c = q.sigmoid ? sigmoid32(l[m]) : expf(l[m] - lmax) / Z;
-      if (q.bias) c += there ? __ldg(q.bias + la.first + la.at(m)) : 0.f;
+      float c = order_score(q.sigmoid, l[m], lmax, rZ);
+      if (q.bias) c += bias[m];
       ck = there ? rank_key(c) : 0u;
       if (q.bias) key[m] = ck;
     }
@@ -389,7 +437,7 @@ __device__ __forceinline__ void select_token(const GateParams& q, long tok) {
     for (int m = 0; m < MAXM; ++m) key[m] = 0u;
   }
 
-  typename Pick<MAXM <= 8, MAXM, VEC>::type offers;
+  typename Pick<(MAXM + 7) / 8, MAXM, VEC>::type offers;
   offers.make(key, la);
   uint32_t my_key = 0, nk = 0;
   int my_e = 0, ne = 0;
@@ -530,12 +578,6 @@ __device__ __forceinline__ uint32_t bits_key(float v) {
   return u ^ ((uint32_t)((int)u >> 31) | 0x80000000u);
 }
 
-__device__ __forceinline__ float rcp_approx(float x) {
-  float r;
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-  return r;
-}
-
 template <int M>
 __global__ void __launch_bounds__(128) k_route_select_many(const GateParams q) {
   constexpr int B = M <= 8 ? 3 : M <= 16 ? 4 : M <= 32 ? 5 : 6;
@@ -577,11 +619,7 @@ __global__ void __launch_bounds__(128) k_route_select_many(const GateParams q) {
     delta = 7.62939453e-6f / Z;  // 2^-17 of the largest score
   }
   const float rZ = rcp_approx(Z);
-  // Scores for the order alone: __expf is off by 2 + 1.173 |x| ulp (x exp(-x) < 0.37) and the reciprocal by
-  // one: a sigmoid by less than 2^-21, a softmax score within its bound above.
-  const auto score = [&](float x) {
-    return q.sigmoid ? rcp_approx(1.f + __expf(-x)) : __expf(x - lmax) * rZ;
-  };
+  const auto score = [&](float x) { return order_score(q.sigmoid, x, lmax, rZ); };
   uint32_t top[8];
 #pragma unroll
   for (int m0 = 0; m0 < M; m0 += 8) {
@@ -744,7 +782,9 @@ cudaError_t launch_many(const GateParams& q, cudaStream_t st) {
 
 template <int MAXM, bool VEC>
 cudaError_t launch_one(const GateParams& q, cudaStream_t st) {
-  const int warps = 8;
+  // small batches: warps on SMs of their own rather than eight to a block
+  const int per_sm = (q.T + num_sms() - 1) / num_sms();
+  const int warps = per_sm < 8 ? per_sm : 8;
   return launch_pdl(k_route_select<MAXM, VEC>, dim3((unsigned)((q.T + warps - 1) / warps)),
                     dim3(32 * warps), 0, st, q);
 }
