@@ -33,10 +33,10 @@ __device__ __forceinline__ void load16(const void* x, int64_t at, float (&v)[16]
   }
 }
 
-// A block takes UNITS * kThreads consecutive units of its slab of kSlab rows (blockIdx.y), a thread every
-// kThreads-th of them, so that its loads are on their way together. Places are 32-bit within a slab, divided
+// A block takes consecutive units of its slab of kSlab rows (blockIdx.y). Places are 32-bit within a slab, divided
 // by multiplication: a 64-bit division a unit took twice the time of the rest.
-constexpr int kThreads = 128;
+constexpr int kQuantThreads = 256;  // of a block (32768 x 7168: 92 us, 128 threads 116, 512 threads 94)
+constexpr int kBackThreads = 128;   // (88 us, 256 threads 93, 512 threads 97)
 constexpr int kSlab = 1 << 16;
 
 struct MxWalk {
@@ -52,81 +52,71 @@ __device__ __forceinline__ uint32_t divided(uint32_t n, const FastDiv& f) {
 
 // Units of 16 elements: half a block of 32. WORDS (K a multiple of 128): the scales of four blocks lie in 8
 // lanes and go out as a word.
-template <bool F32, bool TILES, bool WORDS, int UNITS>
-__global__ void __launch_bounds__(kThreads) k_mx_quantize(const void* __restrict__ x,
+template <bool F32, bool TILES, bool WORDS>
+__global__ void __launch_bounds__(kQuantThreads) k_mx_quantize(const void* __restrict__ x,
                                                           const MxWalk a,
                                                           uint8_t* __restrict__ codes,
                                                           uint8_t* __restrict__ scales) {
   pdl_wait_then_release();
   const long r0 = (long)blockIdx.y * kSlab;
   const uint32_t units = (uint32_t)min(a.rows - r0, (long)kSlab) * a.per.d;
-  const uint32_t u0 = blockIdx.x * (kThreads * UNITS) + threadIdx.x;
+  const uint32_t u = blockIdx.x * kQuantThreads + threadIdx.x;
   const int lane = threadIdx.x & 31, blocks = a.K >> 5;
-  float v[UNITS][16];
-  uint32_t r[UNITS], c[UNITS];
+  const uint32_t r = divided(u, a.per), c = u - r * a.per.d;
+  const long row = r0 + r;
+  float v[16];
+  if (u < units) {
+    load16<F32>(x, row * a.stride + 16 * c, v);
+  } else {
 #pragma unroll
-  for (int i = 0; i < UNITS; ++i) {
-    const uint32_t u = u0 + kThreads * i;
-    r[i] = divided(u, a.per);
-    c[i] = u - r[i] * a.per.d;
-    if (u < units) {
-      load16<F32>(x, (r0 + r[i]) * a.stride + 16 * c[i], v[i]);
-    } else {
-#pragma unroll
-      for (int e = 0; e < 16; ++e) v[i][e] = 0.f;
-    }
+    for (int e = 0; e < 16; ++e) v[e] = 0.f;
   }
+  uint32_t m = 0;
 #pragma unroll
-  for (int i = 0; i < UNITS; ++i) {
-    const uint32_t u = u0 + kThreads * i;
-    uint32_t m = 0;
+  for (int e = 0; e < 16; ++e) m = max(m, __float_as_uint(v[e]) & 0x7FFFFFFFu);
+  m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
+  uint32_t s = scale_byte(m);
+  uint2 w = make_uint2(0, 0);
+  if (s != 255u) {
+    const float f = inverse(s);
+    float h[8];
 #pragma unroll
-    for (int e = 0; e < 16; ++e) m = max(m, __float_as_uint(v[i][e]) & 0x7FFFFFFFu);
-    m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
-    uint32_t s = scale_byte(m);
-    uint2 w = make_uint2(0, 0);
-    if (s != 255u) {
-      const float f = inverse(s);
-      float h[8];
+    for (int e = 0; e < 8; ++e) h[e] = v[e] * f;
+    w.x = codes8(h);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) h[e] = v[i][e] * f;
-      w.x = codes8(h);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) h[e] = v[i][8 + e] * f;
-      w.y = codes8(h);
-    }
-    if (WORDS) {
-      s |= __shfl_down_sync(0xffffffffu, s, 2) << 8;  // of lanes 0, 8, ..: blocks 0, 1; then 2, 3
-      s |= __shfl_down_sync(0xffffffffu, s, 4) << 16;
-    }
-    if (u >= units) continue;
-    const long row = r0 + r[i];
-    reinterpret_cast<uint2*>(codes)[row * a.per.d + c[i]] = w;
-    const int j = (int)(c[i] >> 1);
-    const size_t at = TILES ? tile_at(row, j, a.chunks) : (size_t)row * blocks + j;
-    if (WORDS) {
-      if ((lane & 7) == 0) *reinterpret_cast<uint32_t*>(scales + at) = s;
-    } else if ((lane & 1) == 0) {
-      scales[at] = (uint8_t)s;
-      if (TILES && j == blocks - 1)  // padding of the last chunk: codes beyond K are taken as 0, times 1
-        for (int e = 1; e < 4 - (j & 3); ++e) scales[at + e] = 127;
-    }
+    for (int e = 0; e < 8; ++e) h[e] = v[8 + e] * f;
+    w.y = codes8(h);
+  }
+  if (WORDS) {
+    s |= __shfl_down_sync(0xffffffffu, s, 2) << 8;  // of lanes 0, 8, ..: blocks 0, 1; then 2, 3
+    s |= __shfl_down_sync(0xffffffffu, s, 4) << 16;
+  }
+  if (u >= units) return;
+  reinterpret_cast<uint2*>(codes)[row * a.per.d + c] = w;
+  const int j = (int)(c >> 1);
+  const size_t at = TILES ? tile_at(row, j, a.chunks) : (size_t)row * blocks + j;
+  if (WORDS) {
+    if ((lane & 7) == 0) *reinterpret_cast<uint32_t*>(scales + at) = s;
+  } else if ((lane & 1) == 0) {
+    scales[at] = (uint8_t)s;
+    if (TILES && j == blocks - 1)  // padding of the last chunk: codes beyond K are taken as 0, times 1
+      for (int e = 1; e < 4 - (j & 3); ++e) scales[at + e] = 127;
   }
 }
 
-// Units of 8 elements.
+// Units of 8 elements, every kBackThreads-th of the block's to a thread.
 template <bool F32, bool TILES, int UNITS>
-__global__ void __launch_bounds__(kThreads) k_mx_dequantize(const uint8_t* __restrict__ codes,
+__global__ void __launch_bounds__(kBackThreads) k_mx_dequantize(const uint8_t* __restrict__ codes,
                                                             const uint8_t* __restrict__ scales,
                                                             const MxWalk a, void* __restrict__ y) {
   pdl_wait_then_release();
   const long r0 = (long)blockIdx.y * kSlab;
   const uint32_t units = (uint32_t)min(a.rows - r0, (long)kSlab) * a.per.d;
-  const uint32_t u0 = blockIdx.x * (kThreads * UNITS) + threadIdx.x;
+  const uint32_t u0 = blockIdx.x * (kBackThreads * UNITS) + threadIdx.x;
   uint32_t w[UNITS], s[UNITS], r[UNITS], c[UNITS];
 #pragma unroll
   for (int i = 0; i < UNITS; ++i) {
-    const uint32_t u = u0 + kThreads * i;
+    const uint32_t u = u0 + kBackThreads * i;
     r[i] = divided(u, a.per);
     c[i] = u - r[i] * a.per.d;
     w[i] = s[i] = 0;
@@ -138,7 +128,7 @@ __global__ void __launch_bounds__(kThreads) k_mx_dequantize(const uint8_t* __res
   }
 #pragma unroll
   for (int i = 0; i < UNITS; ++i) {
-    if (u0 + kThreads * i >= units) continue;
+    if (u0 + kBackThreads * i >= units) continue;
     const float f = value(s[i]);
     float v[8];
 #pragma unroll
@@ -186,51 +176,38 @@ __global__ void __launch_bounds__(256) k_mx_tile_scales(const uint8_t* __restric
 
 namespace {
 
-// Matrices that fill the SMs at a unit a thread get several; smaller ones one, and more blocks.
-bool large(const MxRows& r, int unit) {
-  return r.rows * (r.K / unit) > (long)num_sms() * 2048;
-}
-
-MxWalk walk(const MxRows& r, int unit, int units, dim3* grid) {
+MxWalk walk(const MxRows& r, int unit, long block, dim3* grid) {
   MxWalk a{r.rows, r.K, mx_chunks(r.K), r.stride, fast_div((uint32_t)(r.K / unit))};
-  const long slab = r.rows < kSlab ? r.rows : kSlab, block = kThreads * units;
+  const long slab = r.rows < kSlab ? r.rows : kSlab;
   *grid = dim3((unsigned)((slab * (r.K / unit) + block - 1) / block),
                (unsigned)((r.rows + kSlab - 1) / kSlab));
   return a;
 }
 
-template <bool F32, bool TILES, bool WORDS>
-cudaError_t quantize(const MxRows& r, const void* x, uint8_t* codes, uint8_t* scales,
-                     cudaStream_t st) {
-  dim3 grid;
-  if (large(r, 16)) {
-    const MxWalk a = walk(r, 16, 2, &grid);
-    return launch_pdl(k_mx_quantize<F32, TILES, WORDS, 2>, grid, dim3(kThreads), 0, st, x, a, codes,
-                      scales);
-  }
-  const MxWalk a = walk(r, 16, 1, &grid);
-  return launch_pdl(k_mx_quantize<F32, TILES, WORDS, 1>, grid, dim3(kThreads), 0, st, x, a, codes,
-                    scales);
-}
-
 template <bool F32, bool TILES>
 cudaError_t quantize(const MxRows& r, const void* x, uint8_t* codes, uint8_t* scales,
                      cudaStream_t st) {
-  return r.K % 128 == 0 ? quantize<F32, TILES, true>(r, x, codes, scales, st)
-                        : quantize<F32, TILES, false>(r, x, codes, scales, st);
+  dim3 grid;
+  const MxWalk a = walk(r, 16, kQuantThreads, &grid);
+  return r.K % 128 == 0 ? launch_pdl(k_mx_quantize<F32, TILES, true>, grid, dim3(kQuantThreads), 0, st, x,
+                                     a, codes, scales)
+                        : launch_pdl(k_mx_quantize<F32, TILES, false>, grid, dim3(kQuantThreads), 0, st, x,
+                                     a, codes, scales);
 }
 
 template <bool F32, bool TILES>
 cudaError_t dequantize(const MxRows& r, const uint8_t* codes, const uint8_t* scales, void* y,
                        cudaStream_t st) {
   dim3 grid;
-  if (large(r, 8)) {
-    const MxWalk a = walk(r, 8, 4, &grid);
-    return launch_pdl(k_mx_dequantize<F32, TILES, 4>, grid, dim3(kThreads), 0, st, codes, scales, a,
+  // matrices that fill the SMs at a unit a thread get four (32768 x 7168: 95 us with one, 89 with four; in the
+  // other direction, where a unit is 32 bytes, one took 94 us, two 105, four 135)
+  if (r.rows * (r.K / 8) > (long)num_sms() * 2048) {
+    const MxWalk a = walk(r, 8, 4 * kBackThreads, &grid);
+    return launch_pdl(k_mx_dequantize<F32, TILES, 4>, grid, dim3(kBackThreads), 0, st, codes, scales, a,
                       y);
   }
-  const MxWalk a = walk(r, 8, 1, &grid);
-  return launch_pdl(k_mx_dequantize<F32, TILES, 1>, grid, dim3(kThreads), 0, st, codes, scales, a, y);
+  const MxWalk a = walk(r, 8, kBackThreads, &grid);
+  return launch_pdl(k_mx_dequantize<F32, TILES, 1>, grid, dim3(kBackThreads), 0, st, codes, scales, a, y);
 }
 
 }  // namespace
