@@ -134,7 +134,7 @@ __device__ __forceinline__ void group_top2(K& t1, K& t2, int P) {
 // The groups kept, in 64 bits. `least`: what an expert's c in 32 bits has to reach to be one of those that
 // make its group's value; only these are computed again (a lane has one or two of them, as a rule).
 template <int MAXM, bool VEC>
-__device__ __noinline__ bool kept_in_64(const Token<MAXM, VEC>& t, int G, int keep, int group_top,
+__device__ __forceinline__ bool kept_in_64(const Token<MAXM, VEC>& t, int G, int keep, int group_top,
                                         float least, float Z32) {
   const double Z = t.Z64();
   uint64_t todo = 0;
@@ -164,7 +164,7 @@ __device__ __noinline__ bool kept_in_64(const Token<MAXM, VEC>& t, int G, int ke
 
 // The order of the n candidates that lanes 0 .. n-1 hold, in 64 bits: lane r gets the one of rank r.
 template <int MAXM, bool VEC>
-__device__ __noinline__ int ordered_in_64(const Token<MAXM, VEC>& t, int e, int n) {
+__device__ __forceinline__ int ordered_in_64(const Token<MAXM, VEC>& t, int e, int n) {
   const int lane = threadIdx.x & 31;
   const double Z = t.Z64();
   const uint64_t key = lane < n ? rank_key64(t.choice(e, Z)) : 0ull;
@@ -184,7 +184,7 @@ __device__ __noinline__ int ordered_in_64(const Token<MAXM, VEC>& t, int e, int 
 
 // All k rounds in 64 bits: for tokens with more than 32 candidates that fp32 does not tell apart.
 template <int MAXM, bool VEC>
-__device__ __noinline__ int chosen_in_64(const Token<MAXM, VEC>& t, bool kept, int k) {
+__device__ __forceinline__ int chosen_in_64(const Token<MAXM, VEC>& t, bool kept, int k) {
   const int lane = threadIdx.x & 31;
   const double Z = t.Z64();
   uint64_t taken = 0;
@@ -529,8 +529,9 @@ __global__ void __launch_bounds__(256) k_route_select(const GateParams q) {
 // lists of a token are merged to its eight largest in three exchanges. Keys leave values a relative
 // 2^-(23 - B) or 2^-(20 - B), so the eight are ranked in full precision, and the k-th is compared with the
 // largest value that the rest may have. Where those are not apart by their bounds, where group values are
-// not, where a lane has given all its eight, and where a value is NaN or +infinity, the whole warp selects for
-// that token again as above (about two tokens in a hundred at 256 experts).
+// not, where a lane has given all its eight, and where a value is NaN or +infinity, the whole warp selects for that
+// token again as above (a few tokens in a thousand at 256 experts; in a second kernel, with a mark in the first's
+// output, that took longer: 24.1 us for 21.4).
 
 __device__ __forceinline__ void order(uint32_t& a, uint32_t& b) {
   const uint32_t hi = max(a, b), lo = min(a, b);
@@ -579,7 +580,7 @@ __device__ __forceinline__ uint32_t bits_key(float v) {
 }
 
 template <int M>
-__global__ void __launch_bounds__(128) k_route_select_many(const GateParams q) {
+__global__ void __launch_bounds__(128, 7) k_route_select_many(const GateParams q) {
   constexpr int B = M <= 8 ? 3 : M <= 16 ? 4 : M <= 32 ? 5 : 6;
   constexpr uint32_t kLow = (1u << B) - 1u, kLow8 = (8u << B) - 1u;
   constexpr float kRel = 2.f / (float)(1u << (23 - B));    // twice what the last bits stand for
@@ -594,11 +595,34 @@ __global__ void __launch_bounds__(128) k_route_select_many(const GateParams q) {
   const Lane<true> la = lane_of<true>(q, j, q.P >> 2);
   const bool sums = q.keep < q.G && q.group_top == 2;
 
+  // A lane that has a group of its own would read every 16 bytes of another line than its neighbours: its
+  // experts come through shared memory instead (rows padded by 16 bytes: no bank twice), quads of experts
+  // read in a row by the eight lanes (16384 tokens: 3.5 us less).
   float l[M];
+  __shared__ float4 rows[4][32][M / 4 + 1];
+  const bool staged = la.P == 1;
+  if (staged) {
+    float4 (*mine)[M / 4 + 1] = rows[threadIdx.x >> 5];
+    const uint32_t quads = (uint32_t)q.per >> 2, inv = 65536u / quads + 1;  // n / quads, n < 128
+    float4 f[M / 4];
+#pragma unroll
+    for (int i = 0; i < M / 4; ++i) {
+      const uint32_t n = 8 * i + j;
+      if (4 * n < (uint32_t)q.E) f[i] = *reinterpret_cast<const float4*>(lt + 4 * n);
+    }
+#pragma unroll
+    for (int i = 0; i < M / 4; ++i) {
+      const uint32_t n = 8 * i + j, g = (n * inv) >> 16;
+      if (4 * n < (uint32_t)q.E) mine[base + g][n - g * quads] = f[i];
+    }
+    __syncwarp();
+  }
 #pragma unroll
   for (int m = 0; m < M; m += 4) {
     float4 f = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
-    if (la.in && la.at(m) < q.per) f = *reinterpret_cast<const float4*>(lt + la.first + la.at(m));
+    if (la.in && la.at(m) < q.per)
+      f = staged ? rows[threadIdx.x >> 5][lane][m >> 2]
+                 : *reinterpret_cast<const float4*>(lt + la.first + la.at(m));
     l[m] = f.x;
     l[m + 1] = f.y;
     l[m + 2] = f.z;
@@ -820,9 +844,9 @@ cudaError_t launch_route_select(const moe_shape& s, const moe_gate& gate, const 
   const int m = (q.per + q.P * v - 1) / (q.P * v) * v;
   count_launches(1);
   // Eight lanes a token: up to 8 groups and 8 choices, and so many tokens that the warps' share of work counts
-  // and not one warp's latency (with a bias a launch as a rule has a token that is done again, 5 us; measured
-  // at 256 experts in 8 groups: 4096 tokens 13.4 us by warps and 14.9, 16384 tokens 32.6 and 22.3; without a bias
-  // 4099 tokens of 160 experts 7.2 and 5.5).
+  // and not one warp's latency (with a bias a launch as a rule has tokens that are done again, 5 us; measured
+  // at 256 experts in 8 groups: 4096 tokens 11.6 us by warps and 14.9, 6144 tokens 15.6 and 14.0, 16384 tokens 30.9
+  // and 19.3; without a bias 4099 tokens of 160 experts 7.3 and 5.9).
   const int m8 = vec && lanes <= 8 ? (q.per + q.P - 1) / q.P * 4 : 0;  // experts of a lane
   if (m8 && m8 <= 48 && q.k <= 8 && q.T >= (bias ? 6144 : 2048)) {
     if (m8 <= 8) return launch_many<8>(q, st);
