@@ -5,7 +5,8 @@
 Two sequences get their prompts in one ragged step, then tokens one at a time. Every step runs
     h = x + W_o attention(W_qkv norm(x));   y = h + moe(norm(h))
 with AttnLayer (norms, rotation, append, attention) and MoeLayer; the projections are torch
-matrix products. At the end the same tokens go through the block once more, as one prompt a
+matrix products, or MxLinear with `fp4`, when the experts are MXFP4 as well and the router is one of
+sigmoid scores, groups and a selection bias. At the end the same tokens go through the block once more, as one prompt a
 sequence, and the outputs are compared.
 """
 import os
@@ -41,7 +42,7 @@ class PagePool:
 
 class DecoderBlock:
     def __init__(self, d=512, Hq=8, Hkv=2, D=64, E=8, k=2, f=256, kv_dtype="bf16", window=0,
-                 n_sink=0, seed=0):
+                 n_sink=0, fp4=False, seed=0):
         g = torch.Generator(device="cuda").manual_seed(seed)
 
         def w(*shape, scale=0.03):
@@ -56,7 +57,16 @@ class DecoderBlock:
         self.w_qkv, self.w_o = w((Hq + 2 * Hkv) * D, d), w(d, Hq * D)
         self.moe_w = {"wg": w(E, d), "bias": None, "w13": w(E + 1, 2 * f, d), "w2": w(E + 1, d, f),
                       "s13": None, "s2": None}
-        self.moe_layers = {}
+        self.moe_layers, self.fp4 = {}, fp4
+        if fp4:
+            self.qkv = moe.MxLinear.from_weight(self.w_qkv, max_tokens=512)
+            self.out = moe.MxLinear.from_weight(self.w_o, max_tokens=512)
+            self.moe_w["sel_bias"] = torch.randn(E, generator=g, device="cuda") * 0.02
+            for i, rows, K in (("13", 2 * f, d), ("2", d, f)):
+                codes = torch.empty(E + 1, rows, K // 2, dtype=torch.uint8, device="cuda")
+                scales = torch.empty(E + 1, rows, K // 32, dtype=torch.uint8, device="cuda")
+                moe.moe_mx_quantize(moe.mx_rows((E + 1) * rows, K), self.moe_w["w" + i], codes, scales)
+                self.moe_w["w" + i], self.moe_w["s" + i] = codes, scales
 
     def attention(self, **kw):
         return moe.AttnLayer(**self.attn_kw, **kw)
@@ -64,8 +74,9 @@ class DecoderBlock:
     def _moe(self, x):
         T = x.shape[0]
         if T not in self.moe_layers:
-            self.moe_layers[T] = moe.MoeLayer(T, self.d, self.E, self.k, self.f, 1, "bf16",
-                                              self.moe_w)
+            gate = moe.gate_of(n_group=4, topk_group=2, scale=2.5) if self.fp4 else None
+            self.moe_layers[T] = moe.MoeLayer(T, self.d, self.E, self.k, self.f, 1,
+                                              "mxfp4" if self.fp4 else "bf16", self.moe_w, gate=gate)
         return self.moe_layers[T].forward(x)
 
     @staticmethod
@@ -75,6 +86,10 @@ class DecoderBlock:
 
     def step(self, attn, x, table, kv_len, q_start=None):
         """One step of the block: x [T, d] bf16 -> [T, d] bf16."""
+        if self.fp4:
+            qkv = self.qkv.forward(self._norm(x))
+            h = self.out.forward(attn.forward(qkv, table, kv_len, q_start), residual=x)
+            return h + self._moe(self._norm(h))
         qkv = self._norm(x) @ self.w_qkv.T
         h = x + attn.forward(qkv, table, kv_len, q_start) @ self.w_o.T
         return h + self._moe(self._norm(h))
@@ -118,6 +133,6 @@ def run(prompts=(37, 90), steps=6, page_size=16, **kw):
 
 if __name__ == "__main__":
     torch.manual_seed(0)
-    for kw in ({}, {"kv_dtype": "fp8"}, {"window": 48, "n_sink": 4}):
+    for kw in ({}, {"kv_dtype": "fp8"}, {"window": 48, "n_sink": 4}, {"fp4": True}):
         print(kw or "bf16 cache", "steps against whole prompts: largest relative difference",
               f"{run(**kw):.2e}")

@@ -1,6 +1,7 @@
 /*
- * moe.h -- C ABI of the GB300 (sm_103a) routed-expert MoE FFN layer, inference hot path, and of the
- * attention over a paged cache that stands before it in a decoder layer (moe_attn_*, at the end).
+ * moe.h -- C ABI of the GB300 (sm_103a) routed-expert MoE FFN layer, inference hot path, of the
+ * attention over a paged cache that stands before it in a decoder layer (moe_attn_*), and of matrices
+ * in MXFP4 and their product, for the projections around the attention (moe_mx_*).
  *
  * The layer, as the pages state it:
  *   router     -- score every routed expert for each token, keep the top-k
@@ -180,7 +181,8 @@ MOE_API moe_status moe_route_select(const moe_shape* shape, const moe_gate* gate
 
 /* The router from the tokens: moe_route's logits (each in its fixed order, bias added to the logit),
  * then the selection of moe_route_select. x, wg, bias, topk_idx, topk_w, ws as in moe_route (the
- * status word is cleared: a layer starts here). */
+ * status word is cleared: a layer starts here). Every logit is formed in that order at every batch
+ * size; a caller with logits of its own uses moe_route_select. */
 MOE_API moe_status moe_route_gate(const moe_shape* shape, const moe_gate* gate, const void* x,
                                   const void* wg, const float* bias, const float* sel_bias,
                                   int32_t* topk_idx, float* topk_w, void* ws, size_t ws_bytes,

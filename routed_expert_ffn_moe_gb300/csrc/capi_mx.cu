@@ -78,6 +78,8 @@ moe_status moe_mx_quantize(const moe_mx_rows* rows, const void* x, void* codes, 
   REQUIRE_PTR(x, 16);
   REQUIRE_PTR(codes, 16);
   REQUIRE_PTR(scales, 16);
+  if (codes == x || scales == x || codes == scales)
+    return fail(MOE_ERR_INVALID_ARG, "x, codes and scales are arrays of their own");
   cudaError_t e = launch_mx_quantize(r, x, static_cast<uint8_t*>(codes),
                                      static_cast<uint8_t*>(scales),
                                      static_cast<cudaStream_t>(stream));
@@ -93,6 +95,8 @@ moe_status moe_mx_dequantize(const moe_mx_rows* rows, const void* codes, const v
   REQUIRE_PTR(codes, 16);
   REQUIRE_PTR(scales, 16);
   REQUIRE_PTR(y, 16);
+  if (y == codes || y == scales)
+    return fail(MOE_ERR_INVALID_ARG, "y is an array of its own");
   cudaError_t e = launch_mx_dequantize(r, static_cast<const uint8_t*>(codes),
                                        static_cast<const uint8_t*>(scales), y,
                                        static_cast<cudaStream_t>(stream));
@@ -137,6 +141,7 @@ moe_status moe_mx_linear(const moe_mx_shape* shape, const void* x, const void* x
   REQUIRE_PTR(w, 16);
   REQUIRE_PTR(w_scales, 16);
   REQUIRE_PTR(y, 16);
+  if (y == x || y == w) return fail(MOE_ERR_INVALID_ARG, "y is x or w: blocks still read them");
   if (!aligned(bias, 16)) return fail(MOE_ERR_INVALID_ARG, "bias not 16-byte aligned");
   if (!aligned(residual, 16)) return fail(MOE_ERR_INVALID_ARG, "residual not 16-byte aligned");
   if (residual == y && d.r_stride != d.y_stride)

@@ -27,7 +27,7 @@ def test_bad_rows_are_refused(kw, word):
     assert moe.moe_mx_scale_bytes(r) == 0
     for call in (moe.moe_mx_quantize, moe.moe_mx_dequantize):
         with pytest.raises(moe.MoeError) as ei:
-            call(r, F, F, F, stream=0)
+            call(r, F, F + 512, F + 1024, stream=0)
         assert ei.value.status == -1 and word in str(ei.value)
     with pytest.raises(moe.MoeError):
         moe.moe_mx_tile_scales(r, F, F + 512, stream=0)
@@ -48,7 +48,7 @@ def test_quantise_pointers():
     r = moe.mx_rows(4, 64)
     for i, (a, b) in enumerate((("x", "codes"), ("codes", "scales"), ("scales", "y"))):
         for bad, says in ((None, "NULL"), (F + 8, "aligned")):
-            args = [F, F, F]
+            args = [F, F + 512, F + 1024]
             args[i] = bad
             with pytest.raises(moe.MoeError, match=f"{a}.*{says}"):
                 moe.moe_mx_quantize(r, *args, stream=0)
@@ -56,6 +56,12 @@ def test_quantise_pointers():
                 moe.moe_mx_dequantize(r, *args, stream=0)
     with pytest.raises(moe.MoeError, match="same array"):
         moe.moe_mx_tile_scales(r, F, F, stream=0)
+    for args in ((F, F, F + 512), (F, F + 512, F), (F, F + 512, F + 512)):
+        with pytest.raises(moe.MoeError, match="of their own"):
+            moe.moe_mx_quantize(r, *args, stream=0)
+    for args in ((F, F + 512, F), (F, F + 512, F + 512)):
+        with pytest.raises(moe.MoeError, match="of its own"):
+            moe.moe_mx_dequantize(r, *args, stream=0)
     for call in (moe.moe_mx_quantize, moe.moe_mx_dequantize):  # no rows: no call
         call(moe.mx_rows(0, 64), None, None, None, stream=0)
 
@@ -73,7 +79,7 @@ def test_bad_shapes_are_refused(kw, word):
     s = moe.mx_shape(**{**dict(T=4, N=8, K=64), **kw})
     assert moe.moe_mx_linear_workspace_size(s) == 0
     with pytest.raises(moe.MoeError) as ei:
-        moe.moe_mx_linear(s, F, F, F, F, None, None, F, F, stream=0, ws_bytes=1 << 50)
+        moe.moe_mx_linear(s, F, F, F, F, None, None, F + 512, F, stream=0, ws_bytes=1 << 50)
     assert ei.value.status == -1 and word in str(ei.value)
 
 
@@ -81,7 +87,7 @@ def test_linear_pointers():
     for kind in ("bf16", "mxfp4"):
         s = moe.mx_shape(4, 8, 64, kind)
         n = moe.moe_mx_linear_workspace_size(s)
-        good = [F, F if kind == "mxfp4" else None, F, F, None, None, F, F]
+        good = [F, F if kind == "mxfp4" else None, F, F, None, None, F + 512, F]
 
         def refused(at, bad, status=-1, ws_bytes=n):
             args = list(good)
@@ -96,9 +102,10 @@ def test_linear_pointers():
             assert "aligned" in refused(at, F + 8)
         assert "bias" in refused(4, F + 4) and "residual" in refused(5, F + 2)
         assert "workspace" in refused(0, F, -3, n - 1)
+        assert "y is x or w" in refused(6, F)
         assert "x_scales" in refused(1, None if kind == "mxfp4" else F)
     s = moe.mx_shape(4, 8, 64, y_stride=16)
     with pytest.raises(moe.MoeError, match="residual is y"):
-        moe.moe_mx_linear(s, F, None, F, F, None, F, F, F, stream=0, ws_bytes=1 << 20)
+        moe.moe_mx_linear(s, F, None, F, F, None, F + 512, F + 512, F, stream=0, ws_bytes=1 << 20)
     moe.moe_mx_linear(moe.mx_shape(0, 8, 64), None, None, None, None, None, None, None, F, stream=0,
                       ws_bytes=1 << 20)
