@@ -9,6 +9,10 @@
 // that is not kept just stops offering experts. Each of the k rounds takes the warp's largest key;
 // without a bias the key is the logit itself, whose order is that of its score.
 //
+// What bounds it: instructions and their latency. One token takes 4.0 us, most of it one warp's chain; 16384 tokens
+// of 256 experts in 8 groups 19.3 us (2.6 us of reads), 16.8 MB in 4096 warps of 1900 instructions, and 5 us of
+// them the tokens that are done again.
+//
 // Choices next to a border. With a bias (and for sums of two scores) fp32 values may be ordered
 // otherwise than the formulas' values. Each fp32 c lies within delta + 2^-23 |c| of its formula: delta = 2^-20
 // for a sigmoid (order_score and its 1 + e); for softmax the rounding of l - max (2^-24 |l - max|), the
