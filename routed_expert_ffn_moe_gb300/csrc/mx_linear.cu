@@ -18,7 +18,8 @@ namespace {
 
 using namespace mxl;
 
-constexpr int kQuantRows = 4;  // rows of 256 of K that a warp quantises in a block: 4 * 4 in all
+constexpr int kQuantRows = 4;     // rows of 256 of K that a warp quantises in a block: 4 * 4 in all
+constexpr int kQuantStages = 12;  // stages of x beside the ring: two blocks still share an SM
 // Stages whose weights are on their way to L2 before the wait for the kernel ahead: 4 take one token of 9216 x
 // 7168 from 8.0 to 7.3 us; 28, a long row whole, is more than L2 holds over all blocks (65536 x 7168: 50 us for 40).
 constexpr int kAheadStages = 4;
@@ -287,7 +288,9 @@ cudaError_t launch_tile(const CUtensorMap& w, const CUtensorMap& x, const LinPar
   const int nst = (p.chunks + 1) / 2;
   const uint32_t smem = S::total(QUANT ? (nst + p.splits - 1) / p.splits : 0);
   auto kern = k_mx_linear<NT, STAGES, QUANT>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  // the most that any call takes: calls of several host threads do not lower it for each other
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       (int)S::total(QUANT ? kQuantStages : 0));
   if (e != cudaSuccess) return e;
   count_launches(1);
   const dim3 grid((unsigned)tiles * (unsigned)p.splits), block(kLinThreads);
@@ -296,7 +299,6 @@ cudaError_t launch_tile(const CUtensorMap& w, const CUtensorMap& x, const LinPar
              : launch_pdl(kern, grid, block, smem, st, w, x, p);
 }
 
-// Tokens up to which the product's own warps quantise x, so that a call is one launch.
 }  // namespace
 
 cudaError_t launch_mx_linear(const MxDims& d, const void* x, const uint8_t* x_scales,
@@ -321,7 +323,7 @@ cudaError_t launch_mx_linear(const MxDims& d, const void* x, const uint8_t* x_sc
   // 7168 x 7168 7.0 us against 8.1 with a launch ahead; 8 tokens 9.7 against 8.1, as every block quantises its
   // part of x for itself.
   const int nx = (nst + splits - 1) / splits;
-  const bool fused = !d.quantised && nt == 16 && nx <= 12 && d.T * nx <= 4 * kQuantRows;
+  const bool fused = !d.quantised && nt == 16 && nx <= kQuantStages && d.T * nx <= 4 * kQuantRows;
   const uint8_t* codes = static_cast<const uint8_t*>(x);
   if (!d.quantised && !fused) {
     const MxRows r{d.T, d.K, false, true, d.x_stride};

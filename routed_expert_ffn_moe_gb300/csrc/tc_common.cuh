@@ -245,7 +245,13 @@ using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t
                                    const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
                                    CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
 
+// The driver's encoding call, and the device's primary context current in this thread: the call needs one, and
+// a host thread whose first CUDA call it is has none yet (cudaSetDevice makes it current).
 inline EncodeTiledFn encode_fn() {
+  static thread_local int bound = -1;
+  int dev = 0;
+  if (cudaGetDevice(&dev) == cudaSuccess && dev != bound && cudaSetDevice(dev) == cudaSuccess)
+    bound = dev;
   static EncodeTiledFn fn = nullptr;
   if (!fn) {
     void* ptr = nullptr;

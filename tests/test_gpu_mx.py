@@ -344,21 +344,66 @@ def test_repeats_bit_for_bit_and_in_graphs():
         assert ((z.double() - ref2).abs() <= bound(xv, values(wc, wsc), ref2, None, y)).all()
 
 
-def test_weights_written_just_before():
-    """A product right behind the kernel that quantises its weights reads the new ones."""
+@pytest.mark.parametrize("T", [1, 8, 40, 128, 300])
+def test_weights_written_just_before(T):
+    """A product right behind the kernel that quantises its weights reads the new ones, and one behind the
+    kernel that writes its x."""
     t = torch()
-    K, N, T = 2048, 4096, 8
+    K, N = 2048, 4096
     codes = t.zeros(N, K // 2, dtype=t.uint8, device="cuda")
     r = moe.mx_rows(N, K, tiles=True)
     scales = t.zeros(moe.moe_mx_scale_bytes(r), dtype=t.uint8, device="cuda")
     x = t.ones(T, K, dtype=t.bfloat16, device="cuda")
-    shape = moe.mx_shape(T, N, K)
+    xc = t.zeros(T, K // 2, dtype=t.uint8, device="cuda")
+    rx = moe.mx_rows(T, K, tiles=True)
+    xs = t.zeros(moe.moe_mx_scale_bytes(rx), dtype=t.uint8, device="cuda")
+    shape, quantised_shape = moe.mx_shape(T, N, K), moe.mx_shape(T, N, K, "mxfp4")
     ws, y = workspace(shape), t.empty(T, N, dtype=t.bfloat16, device="cuda")
+    z = t.empty_like(y)
     weights = [t.full((N, K), v, dtype=t.bfloat16, device="cuda") for v in (1.0, 2.0, -0.5)]
     for w, v in zip(weights * 3, (1.0, 2.0, -0.5) * 3):
         moe.moe_mx_quantize(r, w, codes, scales)
         moe.moe_mx_linear(shape, x, None, codes, scales, None, None, y, ws)
-        assert (y == K * v).all()
+        moe.moe_mx_quantize(rx, w[:T], xc, xs)
+        moe.moe_mx_linear(quantised_shape, xc, xs, codes, scales, None, None, z, ws)
+        assert (y == K * v).all() and (z == K * v * v).all()
+
+
+def test_host_threads():
+    """Calls of several host threads, with shapes that take different amounts of shared memory."""
+    import threading
+    t = torch()
+    cases = [(1, 300, 4096), (2, 512, 1024), (1, 4096, 6144), (30, 256, 512), (200, 256, 512)]
+    jobs, errors = [], []
+    for i, (T, N, K) in enumerate(cases):
+        wc, wsc = random_mx(N, K, i)
+        x = t.randn(T, K, device="cuda", dtype=t.bfloat16)
+        shape = moe.mx_shape(T, N, K)
+        jobs.append((shape, x, wc, wsc, tiled(wsc), t.empty(T, N, dtype=t.bfloat16, device="cuda"),
+                     workspace(shape), t.cuda.Stream()))
+    t.cuda.synchronize()
+
+    def work(job):
+        shape, x, wc, _, wt, y, ws, st = job
+        try:
+            for _ in range(200):
+                moe.moe_mx_linear(shape, x, None, wc, wt, None, None, y, ws, stream=st)
+        except Exception as e:  # noqa: BLE001
+            errors.append(e)
+
+    threads = [threading.Thread(target=work, args=(j,)) for j in jobs]
+    for th in threads:
+        th.start()
+    for th in threads:
+        th.join()
+    t.cuda.synchronize()
+    assert not errors, errors
+    for _, x, wc, wsc, _, y, ws, _ in jobs:
+        moe.moe_check_device_status(ws)
+        xv = t.from_numpy(quantised(x.double().cpu().numpy())[0]).cuda()
+        wv = values(wc, wsc)
+        ref = xv @ wv.T
+        assert ((y.double() - ref).abs() <= bound(xv, wv, ref, None, None)).all()
 
 
 def test_two_streams():
