@@ -1,7 +1,7 @@
 // y = x w^T + bias + residual, both matrices in MXFP4, on block-scaled tcgen05.mma (kind::mxf4: 64 of
 // K an instruction, one E8M0 scale per row and 32 of K, fp32 sums in TMEM).
 //
-// Up to 128 tokens: the weights are the M side (128 rows a tile), the tokens the N side, so that a single
+// Up to 128 tokens, and more where few tiles have long rows: the weights are the M side (128 rows a tile), the tokens the N side, so that a single
 // token streams each weight byte once at full tile width. A stage holds 256 of K: one 128-byte swizzle row of
 // codes a matrix row and two 512-byte blocks of scales a side, which tcgen05.cp carries to TMEM ahead of the
 // stage's four MMAs. Few tiles are split along K over the CTAs of a cluster; their fp32 sums meet in
@@ -299,6 +299,21 @@ cudaError_t launch_tile(const CUtensorMap& w, const CUtensorMap& x, const LinPar
              : launch_pdl(kern, grid, block, smem, st, w, x, p);
 }
 
+// Whether CTA pairs take the product: for more than 128 tokens, but where few tiles have long rows, which pairs
+// cannot split. Microseconds fitted to x in MXFP4: pairs 3.1 + 0.265 a stage and wave; split tiles 5.3 to 8.5 by the
+// share of the SMs that they fill, and 0.45 a stage of a block. (160 tokens of 128 x 16384: 7.7 by split tiles,
+// 20.0 by pairs; of 4096 x 16384: 14.7 and 21.0; of 4096 x 4096: 9.1 and 7.7.)
+bool by_pairs(const MxDims& d, int tiles, int splits) {
+  if (d.T <= 128) return false;
+  const int nst = (mx_chunks(d.K) + 1) / 2, blocks = tiles * splits, sms = num_sms();
+  const long pair_tiles = (long)((d.T + 255) / 256) * ((d.N + 127) / 128);
+  const long waves = (pair_tiles + sms / 2 - 1) / (sms / 2);
+  const float pairs = 3.1f + 0.265f * (float)nst * (float)waves;
+  const float split = (2 * blocks <= sms ? 5.3f : blocks <= sms ? 6.5f : 8.5f) +
+                      0.45f * (float)((nst + splits - 1) / splits);
+  return blocks > 2 * sms || split + 0.5f >= pairs;
+}
+
 }  // namespace
 
 cudaError_t launch_mx_linear(const MxDims& d, const void* x, const uint8_t* x_scales,
@@ -352,8 +367,7 @@ cudaError_t launch_mx_linear(const MxDims& d, const void* x, const uint8_t* x_sc
   p.vec = d.y_stride % 4 == 0 && (!residual || d.r_stride % 4 == 0);
   p.early = !d.quantised && !fused;
   p.status = reinterpret_cast<int*>(ws + L.status);
-  // many tokens: CTA pairs (256 tokens of 9216 x 7168: 12.5 us against 15.9 here; 128 tokens: 10.9 here)
-  if (d.T > 128) {
+  if (by_pairs(d, tiles, splits)) {
     p.vec = d.y_stride % 8 == 0 && (!residual || d.r_stride % 8 == 0);
     return launch_pair(p, codes, w, st);
   }

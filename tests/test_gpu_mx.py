@@ -258,6 +258,9 @@ def test_full_sizes():
     product(777, 1022, 640, rs=1023, ys=1029, residual=True)
     product(777, 1022, 640, ys=1027, residual=True, alias=True)
     product(4096, 1024, 7168)
+    product(162, 128, 16352, "mxfp4")
+    product(295, 135, 14912, bias=True, residual=True)
+    product(700, 300, 8192)
 
 
 @pytest.mark.parametrize("T", [1, 30, 100, 600])
