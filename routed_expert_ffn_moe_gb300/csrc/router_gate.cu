@@ -251,20 +251,35 @@ struct Offers {
 
 template <int MAXM, bool VEC>
 struct OffersScan {
+  static constexpr int kBlocks = MAXM / 8;  // each with its own best: a win looks through one of them again
   uint32_t key[MAXM];
+  uint32_t block_key[kBlocks];
+  int block_at[kBlocks];
   uint32_t bk;
   int bm, be;
-  __device__ __forceinline__ void find(const Lane<VEC>& la) {
-    bk = 0;
-    bm = 0;
+  __device__ __forceinline__ void look(int b) {
+    block_key[b] = 0;
+    block_at[b] = 8 * b;
 #pragma unroll
-    for (int m = 0; m < MAXM; ++m)
-      if (key[m] > bk) { bk = key[m]; bm = m; }  // of equals the first: a lane's experts ascend
+    for (int i = 0; i < 8; ++i)
+      if (key[8 * b + i] > block_key[b]) {  // of equals the first: a lane's experts ascend
+        block_key[b] = key[8 * b + i];
+        block_at[b] = 8 * b + i;
+      }
+  }
+  __device__ __forceinline__ void find(const Lane<VEC>& la) {
+    bk = block_key[0];
+    bm = block_at[0];
+#pragma unroll
+    for (int b = 1; b < kBlocks; ++b)
+      if (block_key[b] > bk) { bk = block_key[b]; bm = block_at[b]; }
     be = la.first + la.at(bm);
   }
   __device__ __forceinline__ void make(const uint32_t (&k)[MAXM], const Lane<VEC>& la) {
 #pragma unroll
     for (int m = 0; m < MAXM; ++m) key[m] = k[m];
+#pragma unroll
+    for (int b = 0; b < kBlocks; ++b) look(b);
     find(la);
   }
   __device__ __forceinline__ uint32_t best_key() const { return bk; }
@@ -272,7 +287,12 @@ struct OffersScan {
   __device__ __forceinline__ void pop(bool mine, const Lane<VEC>& la) {
     if (mine) {
 #pragma unroll
-      for (int m = 0; m < MAXM; ++m) key[m] = m == bm ? 0u : key[m];
+      for (int b = 0; b < kBlocks; ++b)
+        if (bm >> 3 == b) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) key[8 * b + i] = 8 * b + i == bm ? 0u : key[8 * b + i];
+          look(b);
+        }
       find(la);
     }
     __syncwarp();
