@@ -181,8 +181,10 @@ MOE_API moe_status moe_route_select(const moe_shape* shape, const moe_gate* gate
 
 /* The router from the tokens: moe_route's logits (each in its fixed order, bias added to the logit),
  * then the selection of moe_route_select. x, wg, bias, topk_idx, topk_w, ws as in moe_route (the
- * status word is cleared: a layer starts here). Every logit is formed in that order at every batch
- * size; a caller with logits of its own uses moe_route_select. */
+ * status word is cleared: a layer starts here). The experts are those that all logits in that order
+ * give; large batches form only the logits that the choice depends on (the others by tensor cores, in
+ * the workspace), unless softmax scores need them all: with sel_bias, without renorm, or in sums of two.
+ * A caller with logits of its own uses moe_route_select. */
 MOE_API moe_status moe_route_gate(const moe_shape* shape, const moe_gate* gate, const void* x,
                                   const void* wg, const float* bias, const float* sel_bias,
                                   int32_t* topk_idx, float* topk_w, void* ws, size_t ws_bytes,

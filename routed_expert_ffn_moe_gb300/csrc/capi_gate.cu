@@ -74,8 +74,19 @@ moe_status moe_route_gate(const moe_shape* shape, const moe_gate* gate, const vo
   if (e != cudaSuccess) return cuda_fail(e, "moe_route_gate status reset");
   if (shape->T == 0) return MOE_OK;
   float* logits = reinterpret_cast<float*>(w + L.logits);
-  e = launch_router_logits(*shape, static_cast<const uint16_t*>(x),
-                           static_cast<const uint16_t*>(wg), bias, logits, cs);
+  const uint16_t* xb = static_cast<const uint16_t*>(x);
+  const uint16_t* wb = static_cast<const uint16_t*>(wg);
+  const bool groups = gate->topk_group < gate->n_group;
+  // softmax scores depend on every logit: where they count, all are formed
+  const bool by_logits = gate->score == MOE_SCORE_SIGMOID ||
+                         (!sel_bias && gate->renorm && (!groups || gate->group_top == 1));
+  if (by_logits && router_settles(*shape)) {
+    const SettleRule rule{groups ? gate->n_group : 1, groups ? shape->E / gate->n_group : shape->E,
+                          groups ? gate->topk_group : 1, gate->group_top};
+    e = launch_settled_logits(*shape, xb, wb, bias, sel_bias, rule, w, L, cs);
+  } else {
+    e = launch_router_logits(*shape, xb, wb, bias, logits, cs);
+  }
   if (e == cudaSuccess)
     e = launch_route_select(*shape, *gate, logits, sel_bias, topk_idx, topk_w, cs);
   return e == cudaSuccess ? MOE_OK : cuda_fail(e, "moe_route_gate launch");

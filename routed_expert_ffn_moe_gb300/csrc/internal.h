@@ -102,6 +102,16 @@ cudaError_t launch_router_logits(const moe_shape& s, const uint16_t* x, const ui
                                  const float* bias, float* logits, cudaStream_t st,
                                  int* clear_status = nullptr);
 bool router_uses_tc(const moe_shape& s);
+bool router_settles(const moe_shape& s);
+// The logits of a large batch that a scored selection of this kind depends on (router.cu): groups (G = 1: none),
+// experts of one, groups kept, experts that make a group's value. For sigmoid scores, and for softmax scores where
+// the choice goes by the logits alone.
+struct SettleRule {
+  int G, per, keep, group_top;
+};
+cudaError_t launch_settled_logits(const moe_shape& s, const uint16_t* x, const uint16_t* wg,
+                                  const float* bias, const float* sel, const SettleRule& rule,
+                                  char* ws, const WsLayout& L, cudaStream_t st);
 cudaError_t launch_permute(const moe_shape& s, const int32_t* topk_idx, int32_t* offsets,
                            int32_t* perm_token, int32_t* inv_slot, char* ws, const WsLayout& L,
                            cudaStream_t st);

@@ -8,6 +8,7 @@
 // logits of a token at once. Batches of 1024+ tokens form approximate logits on the tensor
 // cores and recompute only the candidates' logits in the fixed order (same bits; see the
 // section below); hash routing forms only the k hashed logits of each token.
+#include <cfloat>
 #include <cstdlib>
 
 #include "ffn.h"
@@ -256,6 +257,26 @@ __global__ void __launch_bounds__(256) k_router_topk(const float* __restrict__ l
 constexpr float kBoundC = 0x1p-12f;
 constexpr float kNormUp = 1.0f + 0x1p-10f;  // covers the rounding of the fp32 norms
 
+// The norm of a row by a warp, rounded up; 0 for a row of zeros alone. Squares that underflow leave out
+// less than 16384 * 2^-149 of the sum: 2^-60 covers them.
+__device__ __forceinline__ float norm_above(const uint16_t* __restrict__ row, int chunks, int lane) {
+  float ss = 0.f;
+  uint32_t bits = 0u;
+  for (int c = lane; c < chunks; c += 32) {
+    const uint4 v = ldg_u4(row + 8 * c);
+    bits |= (v.x | v.y | v.z | v.w) & 0x7FFF7FFFu;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float f = bf16x8_elem(v, i);
+      ss = fmaf(f, f, ss);
+    }
+  }
+#pragma unroll
+  for (int off = 16; off >= 1; off >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, off);
+  if (!__any_sync(0xffffffffu, bits != 0u)) return 0.f;
+  return ss < 0x1p-100f ? sqrtf(ss) * kNormUp + 0x1p-60f : sqrtf(ss) * kNormUp;
+}
+
 // Block 0 writes the one-matrix tile plan of the logits GEMM (expert offsets {0, T}, tile prefix
 // {0, tiles}) and clears the router's status words; every warp then takes experts e and writes
 // |wg_e| (rounded up).
@@ -275,18 +296,8 @@ __global__ void __launch_bounds__(256) k_router_prep(const uint16_t* __restrict_
   const int chunks = d >> 3;
   for (int e = blockIdx.x * 8 + (threadIdx.x >> 5); e < E; e += gridDim.x * 8) {
     const uint16_t* we = wg + (size_t)e * d;
-    float ss = 0.f;
-    for (int c = lane; c < chunks; c += 32) {
-      const uint4 v = ldg_u4(we + 8 * c);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float f = bf16x8_elem(v, i);
-        ss = fmaf(f, f, ss);
-      }
-    }
-#pragma unroll
-    for (int off = 16; off >= 1; off >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, off);
-    if (lane == 0) wnorm[e] = sqrtf(ss) * kNormUp;
+    const float norm = norm_above(we, chunks, lane);
+    if (lane == 0) wnorm[e] = norm;
   }
 }
 
@@ -379,6 +390,197 @@ __global__ void __launch_bounds__(256) k_router_hash(const uint16_t* __restrict_
     topk_w[(size_t)t * k + lane] = ex / sum;
   }
 }
+
+// The logits that a scored selection (router_gate.cu) depends on, in their defined order, from approximate ones:
+// one warp a token. An expert's value is its logit, or with a selection bias sigmoid(logit) + bias, monotone in
+// the logit, so its interval follows from the logit's.
+//   groups: where these intervals leave open whether a group is kept, the logits of the experts that may make its
+//     value are formed (upper values that reach the group's group_top-th largest lower one); what stays open then
+//     are values next to each other;
+//   experts: of the groups that may be kept, those whose upper value reaches the k-th largest lower value of the
+//     groups that certainly are.
+// Every other expert keeps its approximate logit, whose value lies below what it would have to reach: the selection
+// on this mixture is the selection on the defined logits, and every chosen one is a defined one. A logit that
+// misses its bound has all of the token's formed, as in k_router_select.
+//
+// What bounds it: the router's rows from L2, about 14 experts of 14 KB a token. 16384 tokens of 7168 x 256: 509 us
+// with groups (4 of 8), 378 without, the product before it included; every logit formed 1605. With all groups'
+// best experts formed in every case it was 785, and a token whose groups were next to each other formed all of
+// four groups: 360 us at 1024 tokens. Where all of a token's logits are equal all are formed: 9.5 ms.
+constexpr int kSettleWarps = 4;
+
+__device__ __forceinline__ float settle_sigmoid(float z) {  // within 2^-20
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + __expf(-z)));
+  return r;
+}
+
+__global__ void __launch_bounds__(32 * kSettleWarps) k_router_settle(
+    const uint16_t* __restrict__ x, const uint16_t* __restrict__ wg, const float* __restrict__ bias,
+    const float* __restrict__ sel, float* __restrict__ logits, const float* __restrict__ wnorm, int T,
+    int d, int E, int k, const SettleRule q, float bound_c, int* status) {
+  constexpr unsigned kAll = 0xffffffffu;
+  constexpr int kAtOnce = 4;  // logits formed together
+  extern __shared__ float settle_smem[];
+  pdl_wait_then_release();
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+  const int t = blockIdx.x * kSettleWarps + w;
+  if (t >= T) return;
+  float* lg = settle_smem + w * E;                       // logits
+  float* ep = settle_smem + (kSettleWarps + w) * E;      // their bounds, 0 where formed
+  float* lw = settle_smem + (2 * kSettleWarps + w) * E;  // lower values
+  uint16_t* cand = reinterpret_cast<uint16_t*>(settle_smem + 3 * kSettleWarps * E) + w * E;
+  const uint16_t* xt = x + (size_t)t * d;
+  float* row = logits + (size_t)t * E;
+
+  const float nx = norm_above(xt, d >> 3, lane);
+  for (int e = lane; e < E; e += 32) {
+    const float a = row[e], ah = bias ? __fadd_rn(a, bias[e]) : a;
+    lg[e] = ah;
+    // known without their sum: a masked expert's logit, if the sum is finite, and that of a row of zeros
+    const float wn = wnorm[e], most = __fmul_ru(nx, wn);
+    const bool zero = (nx == 0.f && wn < INFINITY) || (wn == 0.f && nx < INFINITY);
+    ep[e] = zero || (isinf(ah) && !isinf(a) && most < 0x1p126f)
+                ? 0.f
+                : __fadd_ru(__fmul_ru(fmaxf(bound_c, 0.f), most), __fmul_ru(0x1p-22f, fabsf(ah))) + 0x1p-126f;
+  }
+  __syncwarp();
+
+  const auto value = [&](float z, int e) { return sel ? settle_sigmoid(z) + __ldg(sel + e) : z; };
+  const auto slack = [](float v) { return 0x1p-19f + 0x1p-22f * fminf(fabsf(v), FLT_MAX); };
+  const auto lower = [&](int e) {  // a NaN (which ranks last) as -infinity
+    const float v = value(__fsub_rd(lg[e], ep[e]), e);
+    return fmaxf(sel ? v - slack(v) : v, -INFINITY);
+  };
+  const auto upper = [&](int e) {  // a NaN is below nothing
+    const float v = value(__fadd_ru(lg[e], ep[e]), e);
+    return sel ? v + slack(v) : v;
+  };
+  float use = 0.f;
+  bool miss = bound_c < 0.f;
+  // forms the logits of the experts that are wanted (asked of all lanes alike) and not formed yet
+  const auto form = [&](auto wanted) {
+    int n = 0;
+    for (int e0 = 0; e0 < E; e0 += 32) {
+      const int e = e0 + lane;
+      const bool want = wanted(min(e, E - 1)) && e < E && ep[min(e, E - 1)] != 0.f;
+      const unsigned b = __ballot_sync(kAll, want);
+      if (want) cand[n + __popc(b & ((1u << lane) - 1u))] = (uint16_t)e;
+      n += __popc(b);
+    }
+    __syncwarp();
+    for (int g = 0; g < n; g += kAtOnce) {
+      int e[kAtOnce];
+#pragma unroll
+      for (int j = 0; j < kAtOnce; ++j) e[j] = cand[min(g + j, n - 1)];
+      float sum[kAtOnce];
+      defined_logits<kAtOnce>(xt, wg, e, d, lane, sum);
+#pragma unroll
+      for (int j = 0; j < kAtOnce; ++j) {
+        if (g + j >= n) break;
+        const float l = bias ? __fadd_rn(sum[j], bias[e[j]]) : sum[j];
+        const float r = fabsf(l - lg[e[j]]) / ep[e[j]];
+        use = fmaxf(use, r);
+        miss |= !(r <= 1.f);
+        __syncwarp();
+        if (lane == 0) {
+          lg[e[j]] = l;
+          ep[e[j]] = 0.f;
+        }
+      }
+    }
+    __syncwarp();
+  };
+
+  unsigned may = kAll, sure = kAll;  // groups that may be kept, groups that are
+  if (q.keep < q.G) {
+    const auto top2 = [&](float& a, float& b) {  // lane g: the largest two of lw in group g
+      a = b = -INFINITY;
+      __syncwarp();
+      if (lane < q.G)
+        for (int i = 0; i < q.per; ++i) {
+          const float v = lw[lane * q.per + i];
+          b = fmaxf(b, fminf(a, v));
+          a = fmaxf(a, v);
+        }
+      __syncwarp();
+    };
+    const auto group_value = [&](float a, float b) {
+      if (q.group_top == 1) return a;
+      return sel ? a + b : settle_sigmoid(a) + settle_sigmoid(b);
+    };
+    const auto off = [&](float a, float b) {
+      return sel || q.group_top == 2 ? 2.f * (slack(a) + slack(b)) : 0.f;
+    };
+    for (int pass = 0;; ++pass) {
+      float a, b;
+      for (int e = lane; e < E; e += 32) lw[e] = lower(e);
+      top2(a, b);
+      const float least = q.group_top == 2 ? b : a;
+      const float lo = group_value(a, b) - off(a, b);
+      for (int e = lane; e < E; e += 32) {
+        const float v = upper(e);
+        lw[e] = v != v ? INFINITY : v;
+      }
+      top2(a, b);
+      const float hi = group_value(a, b) + off(a, b);
+      int above = 0, not_below = 0;  // other groups, certainly and possibly (a NaN: not known)
+      for (int h = 0; h < q.G; ++h) {
+        const float lo_h = __shfl_sync(kAll, lo, h), hi_h = __shfl_sync(kAll, hi, h);
+        above += lo_h > hi ? 1 : 0;
+        not_below += h != lane && !(hi_h < lo) ? 1 : 0;
+      }
+      may = __ballot_sync(kAll, lane < q.G && above < q.keep);
+      sure = __ballot_sync(kAll, lane < q.G && not_below < q.keep);
+      if (__popc(may) == q.keep) sure = may;
+      if (sure == may || pass == 1) break;
+      const unsigned open = may & ~sure;
+      form([&](int e) {
+        const int g = e / q.per;
+        const float reach = __shfl_sync(kAll, least, g);
+        return ((open >> g) & 1u) && !(upper(e) < reach);
+      });
+    }
+  }
+  const auto in = [&](unsigned groups, int e) { return q.G == 1 || ((groups >> (e / q.per)) & 1u); };
+  // the k-th largest lower value of the groups that are kept: rounds of the next one in the order (value, expert)
+  for (int e = lane; e < E; e += 32) lw[e] = in(sure, e) ? lower(e) : -INFINITY;
+  float theta = INFINITY;
+  int last = -1;
+  for (int j = 0; j < k; ++j) {
+    float bv = -INFINITY;
+    int be = 0x7FFFFFFF;
+    for (int e = lane; e < E; e += 32) {
+      const float v = lw[e];
+      if ((v < theta || (v == theta && e > last)) && v > bv) {
+        bv = v;
+        be = e;
+      }
+    }
+#pragma unroll
+    for (int off = 16; off >= 1; off >>= 1) {
+      const float ov = __shfl_xor_sync(kAll, bv, off);
+      const int oe = __shfl_xor_sync(kAll, be, off);
+      if (ov > bv || (ov == bv && oe < be)) {
+        bv = ov;
+        be = oe;
+      }
+    }
+    theta = bv;
+    last = be;
+  }
+  form([&](int e) { return in(may, e) && !(upper(e) < theta); });
+  if (miss) {
+    for (int e = lane; e < E; e += 32) ep[e] = 1.f;
+    __syncwarp();
+    form([&](int) { return true; });
+    if (lane == 0) atomicAdd(status + kStatusRouterFull, 1);
+  }
+  if (lane == 0) atomicMax(status + kStatusRouterBoundUse, __float_as_int(use));
+  for (int e = lane; e < E; e += 32)
+    if (bias || ep[e] == 0.f) row[e] = lg[e];
+}
+
 
 // One warp per token; lane j holds experts j + 32m, m < MAXM (E <= 32 MAXM). approx holds the
 // tensor-core logits without the bias. Up to 256 experts, two blocks share an SM.
@@ -659,6 +861,17 @@ bool router_uses_tc(const moe_shape& s) {
   return s.E % 128 == 0 && s.d % 64 == 0 && s.E <= 1024 && s.T >= router_tc_min_tokens();
 }
 
+// Forming every logit takes time as T E d; settling has a launch for the norms, a product of few tiles and one
+// warp's chain of logits, which grow with d alone. 8 of 256 experts, groups 4 of 8, forming and settling: 1024 tokens
+// of 7168 123 and 144 us, 2048 223 and 134, 16384 1605 and 509; 4096 tokens of 512 69 and 59; 1024 of 2048 51 and 76.
+// 128 experts of 7168: 2048 tokens 120 and 139, 4096 219 and 144.
+bool router_settles(const moe_shape& s) {
+  if (!router_uses_tc(s)) return false;
+  const char* v = getenv("MOE_ROUTER_TC_MIN_TOKENS");
+  if (v && *v) return true;
+  return (double)s.T * s.E * s.d >= 262144.0 * (s.d + 2048.0);
+}
+
 cudaError_t launch_router_logits(const moe_shape& s, const uint16_t* x, const uint16_t* wg,
                                  const float* bias, float* logits, cudaStream_t st,
                                  int* clear_status) {
@@ -675,9 +888,9 @@ static cudaError_t launch_select(const moe_shape& s, const uint16_t* x, const ui
                     topk_w, status);
 }
 
-static cudaError_t launch_route_tc(const moe_shape& s, const uint16_t* x, const uint16_t* wg,
-                                   const float* bias, int32_t* topk_idx, float* topk_w, char* ws,
-                                   const WsLayout& L, cudaStream_t st) {
+// The plan, the row norms and the approximate logits (without the bias) in the workspace.
+static cudaError_t launch_approx(const moe_shape& s, const uint16_t* x, const uint16_t* wg, char* ws,
+                                 const WsLayout& L, cudaStream_t st) {
   int32_t* plan = reinterpret_cast<int32_t*>(ws + L.rtc);
   float* wnorm = reinterpret_cast<float*>(ws + L.rtc + 16);
   float* approx = reinterpret_cast<float*>(ws + L.logits);
@@ -690,7 +903,7 @@ static cudaError_t launch_route_tc(const moe_shape& s, const uint16_t* x, const 
   cudaError_t e = launch_pdl(k_router_prep, dim3((unsigned)nb), dim3(256), 0, st, wg, s.T, s.d,
                              s.E, tiles, plan, wnorm, status);
   if (e != cudaSuccess) return e;
-  count_launches(2);  // prep and select (launch_tc counts its own)
+  count_launches(1);  // (launch_tc counts its own)
   FfnArgs a{};
   a.T = s.T;
   a.k = 1;
@@ -704,13 +917,41 @@ static cudaError_t launch_route_tc(const moe_shape& s, const uint16_t* x, const 
   a.h = const_cast<uint16_t*>(x);  // read only: the down pass loads its rows through TMA
   a.y_perm = approx;
   a.status = status;
-  e = launch_tc(a, plan + 2, false, true, st);
+  return launch_tc(a, plan + 2, false, true, st);
+}
+
+static cudaError_t launch_route_tc(const moe_shape& s, const uint16_t* x, const uint16_t* wg,
+                                   const float* bias, int32_t* topk_idx, float* topk_w, char* ws,
+                                   const WsLayout& L, cudaStream_t st) {
+  float* wnorm = reinterpret_cast<float*>(ws + L.rtc + 16);
+  float* approx = reinterpret_cast<float*>(ws + L.logits);
+  int* status = reinterpret_cast<int*>(ws + L.status);
+  cudaError_t e = launch_approx(s, x, wg, ws, L, st);
   if (e != cudaSuccess) return e;
+  count_launches(1);
   if (s.E <= 256)
     return launch_select<8>(s, x, wg, bias, approx, wnorm, topk_idx, topk_w, status, st);
   if (s.E <= 512)
     return launch_select<16>(s, x, wg, bias, approx, wnorm, topk_idx, topk_w, status, st);
   return launch_select<32>(s, x, wg, bias, approx, wnorm, topk_idx, topk_w, status, st);
+}
+
+// The logits that a scored selection needs, for large batches (see k_router_settle).
+cudaError_t launch_settled_logits(const moe_shape& s, const uint16_t* x, const uint16_t* wg,
+                                  const float* bias, const float* sel, const SettleRule& rule,
+                                  char* ws, const WsLayout& L, cudaStream_t st) {
+  float* logits = reinterpret_cast<float*>(ws + L.logits);
+  cudaError_t e = launch_approx(s, x, wg, ws, L, st);
+  if (e != cudaSuccess) return e;
+  const size_t smem = (size_t)kSettleWarps * s.E * 14;
+  e = cudaFuncSetAttribute(k_router_settle, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           kSettleWarps * 1024 * 14);
+  if (e != cudaSuccess) return e;
+  count_launches(1);
+  return launch_pdl(k_router_settle, dim3((unsigned)((s.T + kSettleWarps - 1) / kSettleWarps)),
+                    dim3(32 * kSettleWarps), smem, st, x, wg, bias, sel, logits,
+                    reinterpret_cast<const float*>(ws + L.rtc + 16), s.T, s.d, s.E, s.k, rule,
+                    router_tc_bound(), reinterpret_cast<int*>(ws + L.status));
 }
 
 cudaError_t launch_route(const moe_shape& s, const uint16_t* x, const uint16_t* wg,
