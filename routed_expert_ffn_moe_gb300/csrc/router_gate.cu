@@ -553,9 +553,9 @@ __global__ void __launch_bounds__(256) k_route_select(const GateParams q) {
 // lists of a token are merged to its eight largest in three exchanges. Keys leave values a relative
 // 2^-(23 - B) or 2^-(20 - B), so the eight are ranked in full precision, and the k-th is compared with the
 // largest value that the rest may have. Where those are not apart by their bounds, where group values are
-// not, where a lane has given all its eight, and where a value is NaN or +infinity, the whole warp selects for that
-// token again as above (a few tokens in a thousand at 256 experts; in a second kernel, with a mark in the first's
-// output, that took longer: 24.1 us for 21.4).
+// not, where a lane's eight end among those looked at (what it has beside them is in no list), and where a value is
+// NaN or +infinity, the whole warp selects for that token again as above (a few tokens in a thousand at 256 experts;
+// in a second kernel, with a mark in the first's output, that took longer: 24.1 us for 21.4).
 
 __device__ __forceinline__ void order(uint32_t& a, uint32_t& b) {
   const uint32_t hi = max(a, b), lo = min(a, b);
@@ -750,6 +750,7 @@ __global__ void __launch_bounds__(128, 7) k_route_select_many(const GateParams q
 #pragma unroll
   for (int i = 7; i >= 0; --i) ninth = top[i] < best[7] ? max(ninth, top[i]) : ninth;
   ninth = max8(ninth);
+  again |= M > 8 && q.k == 8 && top[7] != 0u && top[7] >= ninth;  // as one whose list ends with the ninth
 #pragma unroll
   for (int i = 7; i >= 0; --i) rest = top[i] < ninth ? max(rest, top[i]) : rest;
   rest = max8(rest);

@@ -1,0 +1,83 @@
+"""Scored routing of large batches where eight lanes share a token: choices whose border runs through the experts
+of one lane, nearer to each other than the keys tell, against the formulas in 64 bits."""
+import numpy as np
+import pytest
+
+import routed_expert_ffn_moe_gb300 as moe
+from test_gpu_gate import MANY, check
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    from routed_expert_ffn_moe_gb300 import build
+    build.build()
+    moe.load()
+
+
+def lane_experts(E, G):
+    """Experts by lane: a group's quads of experts are dealt to the lanes of the group, 8 lanes a token."""
+    lanes = 1
+    while lanes < G:
+        lanes *= 2
+    P, per = 8 // lanes, E // G
+    return [[g * per + e for e in range(per) if e // 4 % P == p] for g in range(G) for p in range(P)]
+
+
+ULP = 2.0 ** -23
+
+
+@pytest.mark.parametrize("biased", [False, True])
+@pytest.mark.parametrize("E,G,keep,top,k", [(256, 8, 2, 1, 8), (256, 1, 1, 2, 8), (256, 8, 8, 2, 8), (96, 1, 1, 2, 8),
+                                            (384, 1, 1, 2, 8), (128, 2, 1, 1, 8), (256, 1, 1, 2, 7), (256, 8, 2, 1, 5)])
+def test_a_border_within_a_lane(E, G, keep, top, k, biased):
+    """A lane that gives up to eight of the k, and two to five more values that lie within the last bits of the k-th's
+    key, its ninth and later ones among them; the rest of the k from other lanes."""
+    r = np.random.default_rng(E + G + k)
+    lanes = lane_experts(E, G)
+    step = r.integers(0, 32, E) if not biased else r.integers(0, 5, E) * 13  # apart by more than the bounds of c
+    l = np.empty((MANY, E), np.float32)
+    for row in l:
+        row[:] = r.uniform(-9, -4.5, E)
+        lane = lanes[r.integers(len(lanes))]
+        near = int(r.integers(2, 6))
+        clear = int(r.integers(0, k))
+        order = np.array(lane)[: clear + near] if r.random() < 0.5 else r.permutation(lane)[: clear + near]
+        of_group = [e for e in range(E) if e // (E // G) == lane[0] // (E // G)]
+        others = r.permutation([e for e in (range(E) if keep > 1 or G == 1 else of_group) if e not in lane])
+        others = others[:max(0, k - clear - 1 - int(r.integers(0, 2)))]
+        high = np.concatenate([order[:clear], others])
+        row[high] = r.uniform(2, 12, len(high)) if not biased else r.uniform(0.5, 4, len(high))
+        row[order[clear:]] = 1 + r.integers(0, 32, len(order) - clear) * ULP if not biased else 0.0
+    bias = (0.5 + step * ULP).astype(np.float32) if biased else None
+    check(l, bias, k, n_group=G, topk_group=keep, group_top=top)
+
+
+def test_the_ninth_ends_a_lane():
+    r = np.random.default_rng(3)
+    l = r.standard_normal((MANY, 256)).astype(np.float32)
+    rows = np.arange(5, MANY, 97)
+    for row in rows:  # groups of 32 experts, one a lane: the ninth of the lane is the eighth of the token
+        l[row] = r.uniform(-9, -4.5, 256)
+        l[row, :6] = np.arange(10, 4, -1)
+        l[row, [6, 7, 8]] = 1 + np.array([10, 5, 20]) * ULP
+        l[row, 40] = 11
+    idx, _ = check(l, None, 8, n_group=8, topk_group=2, group_top=1)
+    assert (idx[rows] == [40, 0, 1, 2, 3, 4, 5, 8]).all()
+    for row in rows:  # no groups
+        l[row] = r.uniform(-9, -4.5, 256)
+        l[row, [0, 1, 2, 3, 32, 33]] = np.arange(10, 4, -1)
+        l[row, [34, 35, 64]] = 1 + np.array([10, 5, 20]) * ULP
+        l[row, 4] = 11
+    idx, _ = check(l, None, 8)
+    assert (idx[rows] == [4, 0, 1, 2, 3, 32, 33, 64]).all()
+    bias = np.full(256, 0.5, np.float32)  # c = sigmoid + bias, 0.5 and a bias of 0.5 and some steps
+    bias[[34, 35, 64]] += (np.array([12, 0, 25]) * ULP).astype(np.float32)
+    for row in rows:
+        l[row] = r.uniform(-9, -4.5, 256)
+        l[row, [0, 1, 2, 3, 32, 33]] = np.linspace(4, 2, 6)
+        l[row, [34, 35, 64]] = 0
+        l[row, 4] = 5
+    idx, _ = check(l, bias, 8)
+    assert (idx[rows] == [4, 0, 1, 2, 3, 32, 33, 64]).all()
