@@ -696,12 +696,15 @@ __global__ void __launch_bounds__(128, 7) k_route_select_many(const GateParams q
   }
 
   if (q.keep < q.G) {
-    const auto val = [](uint32_t key) { return key_logit(key | kLow); };  // not below the true value
+    // not below the true value. Where softmax scores of logits are summed it is cut to the largest logit: a logit
+    // of some millions may be rounded up by more than one, and e^x grows faster than the bound in err
+    const float most = !q.sigmoid && !q.bias && sums ? lmax : INFINITY;
+    const auto val = [most](uint32_t key) { return fminf(key_logit(key | kLow), most); };
     uint32_t t1 = top[0], t2 = top[1];
     group_top2(t1, t2, la.P);
     // v: not below the group's value but for the scores' bounds, nor above it by more than what the last
-    // bits stand for (a score moves by at most a quarter of its logit, or by itself times its logit). One side's
-    // bits and both sides' bounds are in err.
+    // bits stand for (a sigmoid moves by at most a quarter of what its logit does, a softmax score by at most 1 / Z of
+    // it, as e^x <= 1 between the true logit and the cut one). One side's bits and both sides' bounds are in err.
     float v = -INFINITY, err = 0.f;
     if (la.in) {
       const float a = val(t1), b = val(t2), bits = 0.5f * kRel;

@@ -1,5 +1,6 @@
 """Scored routing of large batches where eight lanes share a token: choices whose border runs through the experts
-of one lane, nearer to each other than the keys tell, against the formulas in 64 bits."""
+of one lane, nearer to each other than the keys tell, and groups by softmax scores of logits far from zero, against
+the formulas in 64 bits."""
 import numpy as np
 import pytest
 
@@ -81,3 +82,34 @@ def test_the_ninth_ends_a_lane():
         l[row, 4] = 5
     idx, _ = check(l, bias, 8)
     assert (idx[rows] == [4, 0, 1, 2, 3, 32, 33, 64]).all()
+
+
+@pytest.mark.parametrize("offset", [0.0, 4e4, -4e4, 1e5, 1e6, -1e6, 2.0 ** 21, 2.0 ** 22, -2.0 ** 22, 1e7])
+@pytest.mark.parametrize("E,G,keep", [(64, 8, 1), (256, 8, 4), (384, 8, 3), (128, 4, 2), (160, 2, 1)])
+def test_softmax_groups_far_from_zero(E, G, keep, offset):
+    """Sums of two softmax scores make a group's value, whatever all logits have in common: groups whose best is
+    the largest and whose second is low, against groups with two a little below."""
+    r = np.random.default_rng(int(abs(offset)) % 1000 + E)
+    per, T = E // G, 2050
+    l = np.full((T, E), -1000.0)
+    for g in range(G):
+        at = np.argsort(r.random((T, per)), 1)[:, :2] + g * per
+        alone = r.random(T) < 0.4
+        first = np.where(alone, -r.choice([0.0, 0.25, 1.0], T), -r.choice([0.125, 0.25, 0.5, 0.75, 2.0, 15.0], T))
+        second = np.where(alone, r.choice([-1.0, -2.0, -30.0], T), first - r.choice([0.125, 0.25, 1.0], T))
+        np.put_along_axis(l, at, np.stack([first, second], 1), 1)
+    l = (l + offset).astype(np.float32)
+    check(l, None, 2, score="softmax", n_group=G, topk_group=keep)
+    check(l, None, min(8, keep * per), score="softmax", n_group=G, topk_group=keep, renorm=False)
+
+
+def test_softmax_group_values_of_large_logits():
+    r = np.random.default_rng(11)
+    l = (r.standard_normal((2048, 64)) * 2).astype(np.float32)
+    rows = np.arange(3, 2048, 61)
+    for X in (2.0 ** 21, 2.0 ** 22):
+        for row in rows:
+            l[row] = X - r.uniform(1000, 2000, 64)
+            l[row, [0, 1, 8, 9]] = X - np.array([0, 2, 0.125 if X < 3e6 else 0.5, 0.25 if X < 3e6 else 0.5])
+        idx, _ = check(l, None, 2, score="softmax", n_group=8, topk_group=1)
+        assert (np.sort(idx[rows]) == [8, 9]).all()
