@@ -19,7 +19,8 @@
 // exponential, and a sum of at most 69 roundings: below 2^-17 of the largest score, 1 / Z. Neighbours in the order
 // whose difference is not above the sum of their bounds are computed in 64 bits and ordered again: about two
 // tokens in a thousand at 256 experts with normal logits. Equal logits with equal biases (logits that were
-// rounded to few bits) are exact ties and need no 64 bits.
+// rounded to few bits) are exact ties and need no 64 bits; where the k-th and the first left tie, all experts that
+// do not tie with them are compared with the k-th.
 #include "internal.h"
 #include "router_gate.h"
 #include "topk.cuh"
@@ -103,6 +104,18 @@ struct Token {
   }
   __device__ __forceinline__ double choice(int e, double Z) const {
     return score(e, Z) + (b ? (double)b[e] : 0.0);
+  }
+  // Has the lane an expert within the bounds of ck, the c of expert e, that does not tie with e exactly?
+  __device__ bool others_near(bool kept, int e, float ck, float delta, float rZ) const {
+    bool found = false;
+    for (int m = 0; m < MAXM; ++m)
+      if (kept && la.at(m) < la.per) {
+        const int o = la.first + la.at(m);
+        const float c = order_score(sigmoid, l[o], lmax, rZ) + b[o];
+        if (l[o] != l[e] || b[o] != b[e])
+          found |= fabsf(ck - c) <= 2.f * delta + 1.1920929e-7f * (fabsf(ck) + fabsf(c));
+      }
+    return found;
   }
   __device__ double Z64() const {
     if (sigmoid) return 1.0;
@@ -487,11 +500,15 @@ __device__ __forceinline__ void select_token(const GateParams& q, long tok) {
     const float a = rank_value(my_key), b = rank_value(next_key);
     const float apart = 2.f * delta + 1.1920929e-7f * (finite_abs(a) + finite_abs(b));
     const bool has_next = lane < q.k - 1 || (lane == q.k - 1 && more);
-    bool near = has_next && !(a - b > apart) && !(a == b && fabsf(a) == INFINITY);
-    if (near) near = !(lt[my_e] == lt[next_e] && q.bias[my_e] == q.bias[next_e]);
+    const bool close = has_next && !(a - b > apart) && !(a == b && fabsf(a) == INFINITY);
+    bool near = close;
+    if (close) near = !(lt[my_e] == lt[next_e] && q.bias[my_e] == q.bias[next_e]);
+    const float ck = __shfl_sync(kAll, a, q.k - 1);
+    // a tie of the k-th and the first left: the neighbours that are left stand behind all that tie with them
+    if (__any_sync(kAll, lane == q.k - 1 && close && !near))
+      near |= t.others_near(kept, __shfl_sync(kAll, my_e, q.k - 1), ck, delta, rZ);
     if (__any_sync(kAll, near)) {
       // every expert that may belong among the k: those within the bounds of the k-th's c
-      const float ck = __shfl_sync(kAll, a, q.k - 1);
       int n = q.k;
       bool whole = false;
       while (nk != 0u) {

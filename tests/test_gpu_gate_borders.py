@@ -113,3 +113,19 @@ def test_softmax_group_values_of_large_logits():
             l[row, [0, 1, 8, 9]] = X - np.array([0, 2, 0.125 if X < 3e6 else 0.5, 0.25 if X < 3e6 else 0.5])
         idx, _ = check(l, None, 2, score="softmax", n_group=8, topk_group=1)
         assert (np.sort(idx[rows]) == [8, 9]).all()
+
+
+@pytest.mark.parametrize("T", [1, 3, MANY])
+@pytest.mark.parametrize("score", ["sigmoid", "softmax"])
+@pytest.mark.parametrize("E,G,keep,k", [(16, 1, 1, 4), (64, 1, 1, 8), (64, 4, 2, 5), (256, 8, 4, 8), (384, 1, 1, 6),
+                                        (1000, 1, 1, 8), (60, 5, 3, 32), (66, 6, 2, 7)])
+def test_ties_at_the_border_and_values_near_them(E, G, keep, k, score, T):
+    """Logits of few values, and biases that bring every c to within a rounding of one value: the k-th and the next
+    are exact ties, and behind them experts whose c is larger in the 25th bit and beyond."""
+    r = np.random.default_rng(E + k)
+    for few in (2, 5, 12):
+        l = (r.integers(0, few, (1, E)) * 0.375 - 1).astype(np.float32)
+        x = l[0].astype(np.float64)
+        s = 1 / (1 + np.exp(-x)) if score == "sigmoid" else np.exp(x - x.max()) / np.exp(x - x.max()).sum()
+        b = (0.75 - s).astype(np.float32)
+        check(l.repeat(T, 0), b, k, score=score, n_group=G, topk_group=keep)
