@@ -38,6 +38,8 @@
  *   - Every pointer must be 16-byte aligned (256-byte for ws; 32-byte for MXFP4 w13 and w2).
  *   - Shapes: 1 <= E <= 1024, 1 <= k <= min(E, 32), n_shared in {0, 1}, d and f multiples of
  *     128 with 128 <= d <= 16384 and 128 <= f <= 16384, 0 <= T and T*(k+1) <= 2^30.
+ *   - What a call writes (outputs, ws) overlaps no other array of the call, unless its description
+ *     says so; blocks read and write in any order. moe_mx_* check this and refuse arrays that do.
  *   - Not thread-safe per workspace: calls that share a workspace must be ordered on one stream.
  */
 #ifndef MOE_GB300_H
@@ -438,6 +440,7 @@ MOE_API size_t moe_mx_linear_workspace_size(const moe_mx_shape* shape);
  *            x_scales in tiles.
  *   w        codes [N, K/2], w_scales in tiles.
  *   bias     [N] fp32, or NULL.   residual [T, N] bf16, or NULL; it may be y itself (same stride).
+ *            Columns of one buffer (x, residual and y with the buffer's stride) do not overlap.
  *   y        [T, N] bf16 out.
  * Products are exact, sums are fp32, with one rounding to bf16 at the end. The result does not depend on the
  * order in which blocks run. */

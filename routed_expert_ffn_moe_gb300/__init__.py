@@ -623,7 +623,8 @@ class MxLinear:
     `MxLinear.from_weight`); bias [N] fp32 or None. `forward(x, residual)` takes x [T, K] bf16, whose
     rows may lie apart, and residual [T, N] bf16 or None, at most max_tokens rows, and returns
     y [T, N] bf16: `out`, or the layer's own buffer, which the next forward overwrites. Tensors of
-    another type, size, layout or device raise ValueError.
+    another type, size, layout or device raise ValueError; an `out` that overlaps x, or the residual
+    otherwise than as the same tensor, raises MoeError (other columns of one buffer do not overlap).
     """
 
     def __init__(self, codes, scales, bias=None, max_tokens=4096, device="cuda"):

@@ -1,6 +1,9 @@
 // The C ABI of the MXFP4 operators (include/moe.h): host-side validation and dispatch.
+#include <initializer_list>
+
 #include "capi.h"
 #include "mx.h"
+#include "ranges.h"
 
 namespace moe {
 namespace {
@@ -57,6 +60,31 @@ moe_status check_linear(const moe_mx_shape* s, MxDims* d) {
   return take("r_stride", s->r_stride, s->N, 1, &d->r_stride);
 }
 
+// An array of the call: absent ones overlap nothing.
+struct Array {
+  const char* name;
+  Runs runs;
+  Array(const char* n, const void* p, int64_t bytes) : name(n), runs(p, p ? bytes : 0) {}
+  Array(const char* n, const void* p, int64_t rows, int64_t row_bytes, int64_t step)
+      : name(n), runs(p, p ? rows : 0, row_bytes, step) {}
+};
+
+// Blocks read the inputs while others store: what a call writes lies apart from all else of it.
+moe_status apart(const Array& written, std::initializer_list<Array> others) {
+  for (const Array& o : others)
+    if (overlap(written.runs, o.runs))
+      return fail(MOE_ERR_INVALID_ARG, "%s overlaps %s", written.name, o.name);
+  return MOE_OK;
+}
+
+Array wide_of(const char* name, const void* p, const MxRows& r) {
+  const int64_t size = r.f32 ? 4 : 2;
+  return Array(name, p, r.rows, r.K * size, r.stride * size);
+}
+Array codes_of(const char* name, const void* p, int64_t rows, int K) {
+  return Array(name, p, rows * (K / 2));
+}
+
 }  // namespace
 }  // namespace moe
 
@@ -80,6 +108,9 @@ moe_status moe_mx_quantize(const moe_mx_rows* rows, const void* x, void* codes, 
   REQUIRE_PTR(scales, 16);
   if (codes == x || scales == x || codes == scales)
     return fail(MOE_ERR_INVALID_ARG, "x, codes and scales are arrays of their own");
+  const Array wide = wide_of("x", x, r), c = codes_of("codes", codes, r.rows, r.K);
+  const Array sc("scales", scales, (int64_t)mx_scale_bytes(r));
+  if ((st = apart(c, {wide, sc})) != MOE_OK || (st = apart(sc, {wide})) != MOE_OK) return st;
   cudaError_t e = launch_mx_quantize(r, x, static_cast<uint8_t*>(codes),
                                      static_cast<uint8_t*>(scales),
                                      static_cast<cudaStream_t>(stream));
@@ -97,6 +128,9 @@ moe_status moe_mx_dequantize(const moe_mx_rows* rows, const void* codes, const v
   REQUIRE_PTR(y, 16);
   if (y == codes || y == scales)
     return fail(MOE_ERR_INVALID_ARG, "y is an array of its own");
+  if ((st = apart(wide_of("y", y, r), {codes_of("codes", codes, r.rows, r.K),
+                                       Array("scales", scales, (int64_t)mx_scale_bytes(r))})) != MOE_OK)
+    return st;
   cudaError_t e = launch_mx_dequantize(r, static_cast<const uint8_t*>(codes),
                                        static_cast<const uint8_t*>(scales), y,
                                        static_cast<cudaStream_t>(stream));
@@ -112,6 +146,9 @@ moe_status moe_mx_tile_scales(const moe_mx_rows* rows, const void* scales, void*
   REQUIRE_PTR(scales, 16);
   REQUIRE_PTR(tiles, 16);
   if (scales == tiles) return fail(MOE_ERR_INVALID_ARG, "scales and tiles are the same array");
+  if ((st = apart(Array("tiles", tiles, (int64_t)mx_tile_bytes(r.rows, r.K)),
+                  {Array("scales", scales, r.rows * (r.K / 32))})) != MOE_OK)
+    return st;
   cudaError_t e = launch_mx_tile_scales(r.rows, r.K, static_cast<const uint8_t*>(scales),
                                         static_cast<uint8_t*>(tiles),
                                         static_cast<cudaStream_t>(stream));
@@ -147,6 +184,17 @@ moe_status moe_mx_linear(const moe_mx_shape* shape, const void* x, const void* x
   if (residual == y && d.r_stride != d.y_stride)
     return fail(MOE_ERR_INVALID_ARG, "residual is y but r_stride=%lld is not y_stride=%lld",
                 (long long)d.r_stride, (long long)d.y_stride);
+  const Array ax = d.quantised ? codes_of("x", x, d.T, d.K)
+                               : Array("x", x, d.T, (int64_t)d.K * 2, d.x_stride * 2);
+  const Array axs("x_scales", x_scales, (int64_t)mx_tile_bytes(d.T, d.K));
+  const Array aw = codes_of("w", w, d.N, d.K);
+  const Array aws("w_scales", w_scales, (int64_t)mx_tile_bytes(d.N, d.K));
+  const Array ab("bias", bias, (int64_t)d.N * 4), scratch("ws", ws, (int64_t)L.total);
+  const Array ar("residual", residual == y ? nullptr : residual, d.T, (int64_t)d.N * 2, d.r_stride * 2);
+  const Array ay("y", y, d.T, (int64_t)d.N * 2, d.y_stride * 2);
+  if ((st = apart(ay, {ax, axs, aw, aws, ab, ar, scratch})) != MOE_OK ||
+      (st = apart(scratch, {ax, axs, aw, aws, ab, ar})) != MOE_OK)
+    return st;
   cudaError_t e = launch_mx_linear(
       d, x, static_cast<const uint8_t*>(x_scales), static_cast<const uint8_t*>(w),
       static_cast<const uint8_t*>(w_scales), bias, static_cast<const uint16_t*>(residual),
