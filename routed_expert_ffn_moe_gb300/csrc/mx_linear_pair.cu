@@ -295,8 +295,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
         for (int i = lane; i < kCols; i += 32) bias[i] = feat + i < p.N ? __ldg(p.bias + feat + i) : 0.f;
         __syncwarp();
       }
-      const bool ok =
-          __all_sync(0xffffffffu, wait_phase(acc_full, acc_phase, abort_flag, p.status));
+      bool ok = __all_sync(0xffffffffu, wait_phase(acc_full, acc_phase, abort_flag, p.status));
       if (!ok) {
         if (RES && p.vec && tok0 < p.T && feat < p.N) drain_bar(rbar, res_phase, p.status);
         break;
@@ -318,7 +317,11 @@ __global__ void __launch_bounds__(kPairThreads, 1)
         if (tok0 >= p.T || f0 >= p.N) break;
         if (h) fetch(f0);
         if (RES && p.vec) {
-          wait_phase(rbar, res_phase, abort_flag, p.status);
+          ok = __all_sync(0xffffffffu, wait_phase(rbar, res_phase, abort_flag, p.status));
+          if (!ok) {  // the box in flight lands before the CTA leaves; nothing of it is stored
+            drain_bar(rbar, res_phase, p.status);
+            break;
+          }
           res_phase ^= 1u;
         } else if (p.vec) {
           if (lane == 0) bulk_wait_read();
@@ -358,6 +361,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
           __syncwarp();
         }
       }
+      if (!ok) break;
     }
     if (p.vec && lane == 0) bulk_wait_all();
   }
