@@ -245,22 +245,27 @@ using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t
                                    const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
                                    CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
 
-// The driver's encoding call, and the device's primary context current in this thread: the call needs one, and
-// a host thread whose first CUDA call it is has none yet (cudaSetDevice makes it current).
+// An entry point of the driver, as of CUDA 12.0; NULL if it has none.
+inline void* driver_fn(const char* name) {
+  void* ptr = nullptr;
+  cudaDriverEntryPointQueryResult q;
+  return cudaGetDriverEntryPointByVersion(name, &ptr, 12000, cudaEnableDefault, &q) == cudaSuccess &&
+                 q == cudaDriverEntryPointSuccess
+             ? ptr
+             : nullptr;
+}
+
+// The driver's encoding call, which needs a current context. A thread without one (its first CUDA call, or the
+// context was taken off it) gets the device's primary context, as from any call of the runtime; a context that the
+// caller made current stays.
 inline EncodeTiledFn encode_fn() {
-  static thread_local int bound = -1;
+  using CurrentFn = CUresult (*)(CUcontext*);
+  static const auto current = reinterpret_cast<CurrentFn>(driver_fn("cuCtxGetCurrent"));
+  static const auto fn = reinterpret_cast<EncodeTiledFn>(driver_fn("cuTensorMapEncodeTiled"));
+  CUcontext c = nullptr;
   int dev = 0;
-  if (cudaGetDevice(&dev) == cudaSuccess && dev != bound && cudaSetDevice(dev) == cudaSuccess)
-    bound = dev;
-  static EncodeTiledFn fn = nullptr;
-  if (!fn) {
-    void* ptr = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ptr, 12000, cudaEnableDefault,
-                                         &q) == cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      fn = reinterpret_cast<EncodeTiledFn>(ptr);
-  }
+  const bool has = current && current(&c) == CUDA_SUCCESS && c;
+  if (!has && cudaGetDevice(&dev) == cudaSuccess) cudaSetDevice(dev);
   return fn;
 }
 
