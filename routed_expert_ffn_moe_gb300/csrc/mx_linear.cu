@@ -176,6 +176,9 @@ __global__ void __launch_bounds__(kLinThreads, 2)
         if (++stage == STAGES) { stage = 0; phase ^= 1u; }
       }
       if (ok) mma_commit(acc_full);
+      // where a wait gave up, the MMAs that were issued end before the block leaves
+      for (int s = 0; !ok && s < STAGES; ++s)
+        drain_bar(&empty[s], s < (int)stage ? phase : phase ^ 1u, p.status);
     }
   } else {
     const int w = warp - 2;
