@@ -5,6 +5,7 @@ import numpy as np
 import pytest
 
 import routed_expert_ffn_moe_gb300 as moe
+from gpu_helpers import torch
 from test_gpu_gate import MANY, check
 
 pytestmark = pytest.mark.gpu
@@ -129,3 +130,24 @@ def test_ties_at_the_border_and_values_near_them(E, G, keep, k, score, T):
         s = 1 / (1 + np.exp(-x)) if score == "sigmoid" else np.exp(x - x.max()) / np.exp(x - x.max()).sum()
         b = (0.75 - s).astype(np.float32)
         check(l.repeat(T, 0), b, k, score=score, n_group=G, topk_group=keep)
+
+
+@pytest.mark.parametrize("T", [5119, 5120, 5123])
+def test_batches_around_the_one_that_settles(monkeypatch, T):
+    """The batch from which only the needed logits are formed (512 x 256: 5120 tokens): the choice of all of them."""
+    t = torch()
+    g = t.Generator(device="cuda").manual_seed(T)
+    x = t.randn(T, 512, generator=g, device="cuda", dtype=t.bfloat16)
+    wg = (t.randn(256, 512, generator=g, device="cuda") * 0.1).to(t.bfloat16)
+    sel = t.randn(256, generator=g, device="cuda") * 0.1
+    s, gate = moe.shape_of(T, 512, 256, 8, 128), moe.gate_of(n_group=8, topk_group=4, scale=2.5)
+    ws = t.full((moe.moe_workspace_size(s),), 255, dtype=t.uint8, device="cuda")
+    out = []
+    for least in (None, "1000000000"):  # the rule's own; every logit formed
+        monkeypatch.delenv("MOE_ROUTER_TC_MIN_TOKENS", raising=False)
+        if least:
+            monkeypatch.setenv("MOE_ROUTER_TC_MIN_TOKENS", least)
+        out.append((t.full((T, 8), -7, dtype=t.int32, device="cuda"), t.full((T, 8), -7.0, device="cuda")))
+        moe.moe_route_gate(s, gate, x, wg, None, sel, *out[-1], ws)
+        moe.moe_check_device_status(ws)
+    assert (out[0][0] == out[1][0]).all() and (out[0][1] == out[1][1]).all()
