@@ -9,8 +9,8 @@
 // that is not kept just stops offering experts. Each of the k rounds takes the warp's largest key;
 // without a bias the key is the logit itself, whose order is that of its score.
 //
-// What bounds it: instructions and their latency. One token takes 4.0 us, most of it one warp's chain; 16384 tokens
-// of 256 experts in 8 groups 19.3 us (2.6 us of reads), 16.8 MB in 4096 warps of 1900 instructions, and 5 us of
+// What bounds it: instructions and their latency. One token takes 4.1 us, most of it one warp's chain; 16384 tokens
+// of 256 experts in 8 groups 19.4 us (2.6 us of reads), 16.8 MB in 4096 warps of 1900 instructions, and 5 us of
 // them the tokens that are done again.
 //
 // Choices next to a border. With a bias (and for sums of two scores) fp32 values may be ordered
@@ -891,7 +891,7 @@ cudaError_t launch_route_select(const moe_shape& s, const moe_gate& gate, const 
   // Eight lanes a token: up to 8 groups and 8 choices, and so many tokens that the warps' share of work counts
   // and not one warp's latency (with a bias a launch as a rule has tokens that are done again, 5 us; measured
   // at 256 experts in 8 groups: 4096 tokens 11.6 us by warps and 14.9, 6144 tokens 15.6 and 14.0, 16384 tokens 30.9
-  // and 19.3; without a bias 4099 tokens of 160 experts 7.3 and 5.9).
+  // and 19.4; without a bias 4099 tokens of 160 experts 7.3 and 6.0).
   const int m8 = vec && lanes <= 8 ? (q.per + q.P - 1) / q.P * 4 : 0;  // experts of a lane
   if (m8 && m8 <= 48 && q.k <= 8 && q.T >= (bias ? 6144 : 2048)) {
     if (m8 <= 8) return launch_many<8>(q, st);
