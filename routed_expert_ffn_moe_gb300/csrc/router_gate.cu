@@ -107,14 +107,24 @@ struct Token {
   }
   // Has the lane an expert within the bounds of ck, the c of expert e, that does not tie with e exactly?
   __device__ bool others_near(bool kept, int e, float ck, float delta, float rZ) const {
+    const float le = l[e], be = b[e];
     bool found = false;
-    for (int m = 0; m < MAXM; ++m)
-      if (kept && la.at(m) < la.per) {
-        const int o = la.first + la.at(m);
-        const float c = order_score(sigmoid, l[o], lmax, rZ) + b[o];
-        if (l[o] != l[e] || b[o] != b[e])
-          found |= fabsf(ck - c) <= 2.f * delta + 1.1920929e-7f * (fabsf(ck) + fabsf(c));
+    for (int m0 = 0; m0 < MAXM; m0 += 4) {  // four experts' loads at a time
+      float lo[4], bo[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int at = la.at(m0 + i);
+        const bool there = kept && at < la.per;
+        lo[i] = there ? l[la.first + at] : le;
+        bo[i] = there ? b[la.first + at] : be;
       }
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (lo[i] != le || bo[i] != be) {
+          const float c = order_score(sigmoid, lo[i], lmax, rZ) + bo[i];
+          found |= fabsf(ck - c) <= 2.f * delta + 1.1920929e-7f * (fabsf(ck) + fabsf(c));
+        }
+    }
     return found;
   }
   __device__ double Z64() const {
